@@ -12,7 +12,8 @@
 // 2^(m_old - m_new).  out = O / l, lse = (m - 15 + log2 l) ln 2.  m is the
 // largest t at its last change and changes only when some t passes it by 0.99,
 // so p stays below 2^15.99, within fp16, where the probabilities keep 11 bits
-// down to 2^-29 of the largest and vanish only below 2^-40 of it.
+// down to 2^-29 of the largest and vanish only below 2^-40 of it.  For that the
+// rounding of t and m must stay small beside 0.01 (kFar in kv_device.hpp).
 // NVFP4 queries are bf16 values divided by a power of two per row, which puts
 // the row's largest at 2^14..2^15: exact in fp16 down to 2^-28 of it.
 //
@@ -425,14 +426,20 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
       for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
       mx = fmaxf(quad_max(mx), m);
       // a row without a key so far has m = -inf: any key makes it grow
-      if (__any(mx * c > m * c + kGrow)) {
+      if (__any((mx - m) * c > kGrow)) {
         const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - mx) * c);
         l *= f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= f;
         m = mx;
       }
-      const float shift = m == -INFINITY ? 0.0f : kOffset - m * c;
+      float shift = m == -INFINITY ? 0.0f : kOffset - m * c;
+      if (__any(fabsf(shift) > kFar)) {
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] -= base;
+        shift = kOffset;
+      }
       float e[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {

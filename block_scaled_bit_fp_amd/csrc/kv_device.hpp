@@ -363,8 +363,14 @@ __device__ __forceinline__ void step_end() { __builtin_amdgcn_sched_barrier(0); 
 
 // A key that stands at the maximum has probability 2^kOffset, and the maximum
 // is replaced only by one more than a factor of 2^kGrow larger, which spares
-// some of the rescaling; 2^(kOffset + kGrow) lies within fp16.
-constexpr float kOffset = 15.0f, kGrow = 0.99f;
+// some of the rescaling; 2^(kOffset + kGrow) lies within fp16, with 0.0096 to
+// spare in the exponent.
+// The exponent is fma(S, c, kOffset - m c): the roundings of m c and of the
+// difference, 2^-24 |m c| each, must stay below that, and do up to |m c| = kFar
+// (2^-9 in all).  Where a row of the wave is past it, m is taken off S first,
+// which is exact for the keys near the maximum, the only ones that can pass the
+// bound; for every tile that would be one more instruction per key and row.
+constexpr float kOffset = 15.0f, kGrow = 0.99f, kFar = 16384.0f;
 
 template <int CTRL>
 __device__ __forceinline__ int64_t dpp64(int64_t v) {  // 0 from lanes outside

@@ -482,7 +482,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
         for (int i = 1; i < 32; ++i) mx = fmaxf(mx, sc[i >> 4][i & 15]);
         mx = fmaxf(pair_max(mx), m);
         // a row without a key so far has m = -inf: any key makes it grow
-        if (__any(mx * c > m * c + kGrow)) {
+        if (__any((mx - m) * c > kGrow)) {
           const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - mx) * c);
           l *= f;
 #pragma unroll
@@ -508,7 +508,13 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
               nb_o[x] = nb_now[x];
             }
         }
-        const float shift = m == -INFINITY ? 0.0f : kOffset - m * c;
+        float shift = m == -INFINITY ? 0.0f : kOffset - m * c;
+        if (__any(fabsf(shift) > kFar)) {
+          const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sc[i >> 4][i & 15] -= base;
+          shift = kOffset;
+        }
         // O^T: in steps of 16 keys, 4 half .. + 3 and 8 + 4 half .. + 3 of each
         // in both operands
         const uint16_t* vr = buf.v[at] + (half * 4 + ((lane & 15) >> 2)) * v_stride<D>();
