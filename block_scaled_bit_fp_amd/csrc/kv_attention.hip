@@ -208,7 +208,7 @@ constexpr int wgs_per_cu(int mode, int D) {
 
 template <int MODE, int D>
 __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel(KvParams p, KvParts parts) {
-  constexpr int W = D / 32, DT = D / 16, G64 = D / 64;
+  constexpr int W = D / 32, DT = D / 16, G64 = D / 64, kFlags = kGroupFlags<MODE, D>;
   __shared__ __align__(16) uint8_t lds[split_lds_bytes<D>()];
   __shared__ float s_ml[kWaves][2][kRows];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, qd = lane >> 4;
@@ -389,6 +389,23 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
 #pragma unroll
             for (int j = 0; j < W; ++j) v.c[u].w[j] = 0;
             v.s[u] = 0;
+          }
+        }
+        if constexpr (kFlags > 0) {
+          const uint32_t bad[2] = {not_finite<MODE>(v.s[0]), not_finite<MODE>(v.s[1])};
+          if (q.q_len > 1 && __any(bad[0] | bad[1])) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t seen = keys_seen(key0 + u * 16, lo, hi);
+#pragma unroll
+              for (int j = 0; j < kFlags; ++j) {
+                const uint64_t keys = __ballot(bad[u] >> (8 * j + 7) & 1u);
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                  if (d % kFlags == j) o[d] += (uint32_t)(keys >> (d * 64 / D * 16)) & seen ? NAN : 0.0f;
+              }
+              v.s[u] = without<MODE>(v.s[u], bad[u]);
+            }
           }
         }
       }

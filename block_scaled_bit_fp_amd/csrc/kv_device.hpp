@@ -231,6 +231,36 @@ __device__ __forceinline__ int value_exponent(uint32_t scales) {
   }
 }
 
+// Values that are not finite: NVFP4 groups whose scale is E4M3's NaN, affine
+// ones with a scale or bias that is not finite (kv_append writes such groups
+// where the input holds an infinity, and all their values are NaN).  Bit 7 of
+// byte j: of group j of the lane's quarter.  MXFP4 has none: every E8M0 byte
+// is taken for a power of two.
+// A probability of zero does not take such a value out of a sum, so in tiles
+// with keys that some rows see and others do not, the values are taken as zero
+// and the rows that see them get NaN in those columns.
+template <int MODE>
+__device__ __forceinline__ uint32_t not_finite(uint32_t scales) {
+  if constexpr (MODE == BSFP_NVFP4) {
+    return ((scales & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  } else if constexpr (MODE == BSFP_AFFINE) {
+    const float s = bf16_lo(scales), b = bf16_hi(scales);
+    return fabsf(s) < INFINITY && fabsf(b) < INFINITY && fabsf(__builtin_fmaf(15.0f, s, b)) < INFINITY
+               ? 0u : 0x80u;
+  } else {
+    return 0u;
+  }
+}
+// Groups that it tells apart per quarter of a row.
+template <int MODE, int D>
+constexpr int kGroupFlags = MODE == BSFP_NVFP4 ? D / 64 : MODE == BSFP_AFFINE ? 1 : 0;
+// The scales with those groups' taken as zero.
+template <int MODE>
+__device__ __forceinline__ uint32_t without(uint32_t scales, uint32_t flags) {
+  if constexpr (MODE == BSFP_NVFP4) return scales & ~((flags >> 7) * 0xFFu);
+  else return flags ? 0u : scales;
+}
+
 // Exponents at which the scaled values stand: the largest is put at 2^8, and
 // room is made again when one would pass 2^13 (6 * 2^13 < 65504).
 constexpr int kValueExp = 127 + 8, kValueExpMax = 127 + 13;
@@ -348,6 +378,12 @@ __device__ __forceinline__ void row_keys(const KvParams& p, const KvRequest& q, 
   const int pos = q.kv - q.q_len + i;
   hi = pos < 0 ? 0 : min(pos, q.last - 1) + 1;
   lo = p.window && pos >= p.window ? pos - p.window + 1 : 0;
+}
+
+// Bit i: key + i lies in [lo, hi), for 16 keys.
+__device__ __forceinline__ uint32_t keys_seen(int key, int lo, int hi) {
+  const int a = min(max(lo - key, 0), 16), b = min(max(hi - key, 0), 16);
+  return ((1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
 // ------------------------------------------------------- workgroups

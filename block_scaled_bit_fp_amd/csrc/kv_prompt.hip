@@ -152,13 +152,14 @@ template <int D>
 struct Row {
   Words<D / 32> w;
   uint32_t s;
-  bool ok;
+  bool ok, parted;  // bits 0 and 1 of s_ok; parted is the same in all lanes
 };
 
 template <int MODE, int D>
 __device__ __forceinline__ void load_row(const KvParams& p, const KvSide& side, int head, int key,
                                          int page, int qd, Row<D>& r) {
   r.ok = page >= 0 && page < p.pages;
+  r.parted = false;
   const int64_t row = cache_row(p, r.ok ? page : 0, head, key & ((1 << p.page_shift) - 1));
   constexpr int B = scale_bytes<MODE, D>();
   r.w = load_codes<D>(side.codes + row * (D / 2), 0, qd);
@@ -170,11 +171,16 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
                                                                               KvParts parts) {
   constexpr int W = D / 32, KS = D / 16, DT = D / 32, G64 = D / 64;
   constexpr bool kAffine = MODE == BSFP_AFFINE;
+  constexpr int kFlags = kGroupFlags<MODE, D>;
   __shared__ __align__(16) Buffers<D> buf;
   __shared__ float s_scale[kAffine ? 2 : 1][kAffine ? G64 : 1][kTile];
   __shared__ float s_bias[kAffine ? 2 : 1][kAffine ? G64 : 1][kTile];
   __shared__ int s_exp[2][4][kWaves];
-  __shared__ uint32_t s_ok[2];  // a byte for each 16 keys
+  // a byte for each 16 keys (a wave stages them).  Bit 0: their page is one of
+  // the cache's.  Bit 1: some of their values are not finite and taken as zero;
+  // s_bad: lane 4 (key % 16) + quarter of the columns, by group of the quarter
+  __shared__ uint32_t s_ok[2];
+  __shared__ uint64_t s_bad[2][kFlags ? kFlags : 1][kWaves];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int skey = tid >> 2, sq = tid & 3;  // the thread's part of a tile
@@ -308,6 +314,8 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
     int lo, hi;
     row_keys(p, q, qi, lo, hi);
     const Reach all = reach(p, q, block * kBlock, block * kBlock + block_rows);
+    // the tiles that every row of the block sees whole
+    const int full0 = (all.all_lo + kTile - 1) / kTile, full1 = all.all_hi / kTile;
     const Reach mine = wave_rows ? reach(p, q, first_row, first_row + wave_rows) : Reach{};
 
     f32x16_t o[DT];
@@ -316,6 +324,8 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
     float m = -INFINITY, l = 0.0f;
+    // bit 4 j + quarter: the row sees a value of that group that is not finite
+    uint32_t nans = 0;
     // V of quarter x of the columns is held times 2^nb: in O, in the tile in use
     // and in the tile being staged
     int nb_o[4] = {0, 0, 0, 0}, nb_now[4] = {0, 0, 0, 0}, nb_next[4] = {0, 0, 0, 0};
@@ -344,6 +354,23 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
           if (!have_nb || e + nb_next[x] > kValueExpMax) nb_next[x] = value_shift(e);
         }
         have_nb = true;
+      }
+    };
+    // Before tile t is staged; tiles that all rows see whole go without.
+    auto part_values = [&](Row<D>& r, int t) {
+      if constexpr (kFlags > 0) {
+        if (t >= full0 && t < full1) return;
+        const int key = t * kTile + skey;
+        const uint32_t bad =
+            r.ok && key >= all.any_lo && key < all.any_hi ? not_finite<MODE>(r.s) : 0u;
+        if (!__any(bad)) return;
+#pragma unroll
+        for (int j = 0; j < kFlags; ++j) {
+          const uint64_t lanes = __ballot(bad >> (8 * j + 7) & 1u);
+          if (lane == 0) s_bad[t & 1][j][wave] = lanes;
+        }
+        r.parted = true;
+        r.s = without<MODE>(r.s, bad);
       }
     };
     auto stage_k = [&](const Row<D>& r, int t, int j0, int j1) {  // words [j0, j1)
@@ -377,7 +404,8 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
       for (int j = j0; j < j1; ++j)
         *reinterpret_cast<u32x4_t*>(vr + v_piece<D>(sq, j) * 8) =
             decode_value_word<MODE, D>(seen ? r.w.w[j] : 0u, vs, j, nb);
-      if (j0 == 0 && (tid & 63) == 0) reinterpret_cast<uint8_t*>(&s_ok[at])[skey >> 4] = r.ok;
+      if (j0 == 0 && lane == 0)
+        reinterpret_cast<uint8_t*>(&s_ok[at])[wave] = r.ok | (kFlags > 0 && r.parted) << 1;
     };
     // The columns 16 j .. of the keys 32 u .. of tile t, as an operand.
     auto key_operand = [&](int at, int i) {
@@ -423,6 +451,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
     publish(rv, t);
     if constexpr (MODE != BSFP_NVFP4) __syncthreads();
     settle(t);
+    part_values(rv, t);
     stage_k(rk, t, 0, W);
     stage_v(rv, t, 0, W);
     load_row<MODE, D>(p, p.k, head, (t + 1) * kTile + skey, page, sq, rk);
@@ -435,6 +464,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
 #pragma unroll
       for (int x = 0; x < 4; ++x) nb_now[x] = nb_next[x];
       settle(t + 1);
+      part_values(rv, t + 1);
       auto load = [&]() {
         load_row<MODE, D>(p, p.k, head, (t + 2) * kTile + skey, page, sq, rk);
         load_row<MODE, D>(p, p.v, head, (t + 2) * kTile + skey, page, sq, rv);
@@ -468,6 +498,26 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
         load();
         const uint32_t ok = __builtin_amdgcn_readfirstlane(s_ok[at]);
         if (key0 < mine.all_lo || key0 + kTile > mine.all_hi || ok != 0x01010101u) {
+          if constexpr (kFlags > 0) {
+            if (ok & 0x02020202u) {
+#pragma unroll
+              for (int j = 0; j < kFlags; ++j) {
+                uint64_t quarters = 0;  // four bits a key
+#pragma unroll
+                for (int x = 0; x < kWaves; ++x) {
+                  const int z0 = min(max(lo - key0 - x * 16, 0), 16);
+                  const int z1 = min(max(hi - key0 - x * 16, z0), 16);
+                  const uint64_t seen = z1 > z0 ? ~0ull >> (64 - 4 * (z1 - z0)) << (4 * z0) : 0;
+                  if (ok >> (x * 8) & 2u) quarters |= s_bad[at][j][x] & seen;
+                }
+                uint32_t y = (uint32_t)quarters | (uint32_t)(quarters >> 32);
+                y |= y >> 16;
+                y |= y >> 8;
+                y |= y >> 4;
+                nans |= (y & 15u) << (4 * j);
+              }
+            }
+          }
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -576,6 +626,14 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
             if (d / (D / 128) == x) o[d] *= f;
           }
         }
+      }
+    }
+    if constexpr (kFlags > 0) {
+#pragma unroll
+      for (int d = 0; d < 2 * DT; ++d) {  // 16 columns
+        const float y = nans >> (d % kFlags * 4 + d * 64 / D) & 1u ? NAN : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[d / 2][(d & 1) * 8 + i] += y;
       }
     }
     const bool whole = b - a == tiles;

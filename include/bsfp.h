@@ -417,7 +417,8 @@ bsfp_status bsfp_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* 
  * with K, V the values the cache stands for.  Query head h reads kv head
  * h / (heads / kv_heads).  A row that sees no key gives out = 0 and
  * lse = -inf, and so do rows of `out` at or past q_starts[requests].  What
- * the pages hold beyond a request's keys has no effect.
+ * the pages hold beyond a request's keys has no effect, and a key none on the
+ * rows that do not see it, NaN and infinities among its values included.
  *   q [tokens, heads, head_dim] bf16, q_stride elements from token to token
  *   out [tokens, heads, head_dim] bf16 contiguous; lse [tokens, heads] fp32
  *   or NULL

@@ -1,11 +1,12 @@
-"""kv_attention where values are extreme: logits of 1e5 and more.  Against fp64 over the values that the cache
-stands for, with the tolerances of kv_reference.py."""
+"""kv_attention where values are extreme: logits of 1e5 and more, and values that are not finite at keys
+that only some rows of a request see.  Against fp64 over the values that
+the cache stands for, with the tolerances of kv_reference.py."""
 import numpy as np
 import pytest
 import torch
 
 import kv_reference as ref
-from test_gpu_kv import MODES, NVFP4, build, new_cache, rand
+from test_gpu_kv import AFFINE, MODES, NVFP4, build, new_cache, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,59 @@ def test_large_finite_logits_stay_finite(bsfp, mode, kv, q_lens, logit):
         assert (np.abs(out - wout) <= otol).all()
         # where that tolerance says little: a mean of values, and no larger than the largest of them
         assert np.abs(out).max() < 8.0
+
+
+def reach_of(batch, q_lens, r):
+    """The position of the request's first new token."""
+    return int(batch.kv_lens[r]) - q_lens[r]
+
+
+@pytest.mark.parametrize("mode", [NVFP4, AFFINE])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kv,q_lens,heads,window", [
+    ([100, 61], [4, 7], 4, 0), ([100, 40], [16, 3], 1, 5), ([260, 200], [70, 40], 4, 0), ([300, 129], [129, 60], 1, 0),
+    ([300, 129], [129, 60], 2, 20), ([2100], [5], 2, 0), ([1500], [12], 4, 0)])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(bsfp, mode, D, kv, q_lens, heads, window):
+    """One key of the new tokens holds NaN and infinities in one group of its values: rows before it (or
+    past its window) are those of a cache without it, rows that see it are not finite there."""
+    P = 32
+    cache, batch, q = build(bsfp, mode, kv, q_lens, heads, 1, D, P, seed=D + heads)
+    clean = bsfp.kv_attention(q, cache, batch, window=window, return_lse=True)
+    starts = np.concatenate([[0], np.cumsum(q_lens)])
+    G = 64 if mode == AFFINE else 16
+    want = clean[0].clone()
+    bad_rows = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
+    group = D // G - 1
+    for r in range(len(kv)):
+        t = reach_of(batch, q_lens, r) + q_lens[r] // 2  # seen by the later half of the rows
+        row = int(batch.block_table[r, t // P]) * P + t % P
+        if mode == AFFINE:
+            cache.v.scales[row, group] = float("inf")
+            cache.v.biases[row, group] = float("nan")
+        else:
+            cache.v.scales[row, group] = 0x7F
+        pos = torch.arange(q_lens[r], device="cuda") + reach_of(batch, q_lens, r)
+        sees = pos >= t
+        if window:
+            sees &= pos < t + window
+        bad_rows[starts[r]:starts[r + 1]] = sees
+    out, lse = bsfp.kv_attention(q, cache, batch, window=window, return_lse=True)
+    assert torch.equal(lse, clean[1])
+    cols = slice(group * G, group * G + G)
+    assert torch.equal(out[~bad_rows], want[~bad_rows])
+    assert torch.isnan(out[bad_rows][..., cols]).all()
+
+
+def test_infinite_inputs_reach_only_the_rows_that_see_them(bsfp):
+    """The same through kv_append: an affine row with an infinity has no finite scale."""
+    for kv, q_lens in (([90], [5]), ([400], [150])):
+        cache, batch, q = build(bsfp, AFFINE, kv, q_lens, 2, 1, 128, 64, seed=5)
+        clean = bsfp.kv_attention(q, cache, batch)
+        t = kv[0] - 2
+        v = rand((1, 1, 128), 9)
+        v[0, 0, 3] = float("inf")
+        slot = batch.block_table[0, t // 64].long().view(1) * 64 + t % 64
+        bsfp.kv_append(cache, rand((1, 1, 128), 10), v, slot)
+        out = bsfp.kv_attention(q, cache, batch)
+        assert torch.equal(out[:-2], clean[:-2])
+        assert not torch.isfinite(out[-2:, :, :64]).any() and torch.isfinite(out[-2:, :, 64:]).all()
