@@ -9,7 +9,7 @@
 //
 // Softmax in one pass.  With t = S scale log2 e and m a running bound of t,
 // p = 2^(t - m + 15); a new m multiplies the sum l and the accumulators O by
-// 2^(m_old - m_new).  out = O / l, lse = (m - 15 + log2 l) ln 2.  m is the
+// 2^(m_old - m_new).  out = O / l, lse = (m + log2 (l / 2^15)) ln 2.  m is the
 // largest t at its last change and changes only when some t passes it by 0.99,
 // so p stays below 2^15.99, within fp16, where the probabilities keep 11 bits
 // down to 2^-29 of the largest and vanish only below 2^-40 of it.  For that the
@@ -492,12 +492,10 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
     }
 
     // ---- join the waves
-    if constexpr (MODE != BSFP_NVFP4) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-        o[d] *= ldexpf(1.0f, -__builtin_amdgcn_readlane(nb, (d * 64 / D) * 16));
-    }
-    l = quad_sum(l);
+    for (int d = 0; d < DT; ++d)
+      o[d] *= ldexpf(1.0f, -kOffsetExp - __builtin_amdgcn_readlane(nb, (d * 64 / D) * 16));
+    l = quad_sum(l) * ldexpf(1.0f, -kOffsetExp);
     const float mt = m == -INFINITY ? -INFINITY : m * c;
     if (single) {
       if (live) {

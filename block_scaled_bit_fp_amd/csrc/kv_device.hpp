@@ -406,7 +406,10 @@ __device__ __forceinline__ void step_end() { __builtin_amdgcn_sched_barrier(0); 
 // (2^-9 in all).  Where a row of the wave is past it, m is taken off S first,
 // which is exact for the keys near the maximum, the only ones that can pass the
 // bound; for every tile that would be one more instruction per key and row.
-constexpr float kOffset = 15.0f, kGrow = 0.99f, kFar = 16384.0f;
+// At the end of a segment's part O and l are divided by 2^kOffset, so that sums
+// of values near the end of bf16's range do not pass fp32's.
+constexpr int kOffsetExp = 15;
+constexpr float kOffset = kOffsetExp, kGrow = 0.99f, kFar = 16384.0f;
 
 template <int CTRL>
 __device__ __forceinline__ int64_t dpp64(int64_t v) {  // 0 from lanes outside
@@ -499,9 +502,9 @@ __device__ __forceinline__ Run find_run(const KvRequests& reqs, int run, int run
   return x;
 }
 
-// lse from the maximum (times log2 e, offset in) and the sum.
+// lse from the maximum (times log2 e) and the sum.
 __device__ __forceinline__ float row_lse(float m, float l) {
-  return l == 0.0f ? -INFINITY : (m - kOffset + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+  return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------- partial states

@@ -609,22 +609,20 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
     }
 
     // ---- out, or the partial state
-    l = pair_sum(l);
+    l = pair_sum(l) * ldexpf(1.0f, -kOffsetExp);
     const float mt = m == -INFINITY ? -INFINITY : m * c;
-    if constexpr (MODE != BSFP_NVFP4) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float f = ldexpf(1.0f, -nb_o[x]);
+    for (int x = 0; x < 4; ++x) {
+      const float f = ldexpf(1.0f, -kOffsetExp - nb_o[x]);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          if constexpr (D == 64) {
-            if (d == x / 2) {
+      for (int d = 0; d < DT; ++d) {
+        if constexpr (D == 64) {
+          if (d == x / 2) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) o[d][(x & 1) * 8 + i] *= f;
-            }
-          } else {
-            if (d / (D / 128) == x) o[d] *= f;
+            for (int i = 0; i < 8; ++i) o[d][(x & 1) * 8 + i] *= f;
           }
+        } else {
+          if (d / (D / 128) == x) o[d] *= f;
         }
       }
     }

@@ -1,12 +1,12 @@
-"""kv_attention where values are extreme: logits of 1e5 and more, and values that are not finite at keys
-that only some rows of a request see.  Against fp64 over the values that
+"""kv_attention where values are extreme: logits of 1e5 and more, values near the end of bf16's range, and
+values that are not finite at keys that only some rows of a request see.  Against fp64 over the values that
 the cache stands for, with the tolerances of kv_reference.py."""
 import numpy as np
 import pytest
 import torch
 
 import kv_reference as ref
-from test_gpu_kv import AFFINE, MODES, NVFP4, build, new_cache, rand
+from test_gpu_kv import AFFINE, MODES, MXFP4, NVFP4, build, check_attention, new_cache, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,16 @@ def test_infinite_inputs_reach_only_the_rows_that_see_them(bsfp):
         out = bsfp.kv_attention(q, cache, batch)
         assert torch.equal(out[:-2], clean[:-2])
         assert not torch.isfinite(out[-2:, :, :64]).any() and torch.isfinite(out[-2:, :, 64:]).all()
+
+
+@pytest.mark.parametrize("mode", [MXFP4, AFFINE])
+@pytest.mark.parametrize("kv,q_lens", LAYOUTS)
+def test_values_near_the_end_of_the_range(bsfp, mode, kv, q_lens):
+    """Means of values of 2^112 to 2^118 are finite."""
+    cache, batch, q = build(bsfp, mode, kv, q_lens, 4, 2, 128, 64, seed=31)
+    for r, n in enumerate(kv):
+        t = torch.arange(n, device="cuda")
+        slots = batch.block_table[r, t // 64].long() * 64 + t % 64
+        v = (rand((n, 2, 128), 50 + r).float().clamp(-4, 4) * 2.0 ** 115).to(torch.bfloat16)
+        bsfp.kv_append(cache, rand((n, 2, 128), 60 + r), v, slots)
+    check_attention(bsfp, cache, batch, q)
