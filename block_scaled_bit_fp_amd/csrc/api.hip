@@ -10,6 +10,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <iterator>
 #include <mutex>
 
 #include "bsfp_device.hpp"
@@ -507,6 +508,16 @@ static bsfp_status check_kv_cache(const bsfp_kv_cache* c, const char* fn) {
   return ok();
 }
 
+struct Range {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+static bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+
 bsfp_status bsfp_kv_plan(const int32_t* past_lens, const int32_t* q_lens, int32_t requests,
                          int32_t page_size, int32_t* block_table, int32_t max_pages,
                          const int32_t* free_pages, int64_t free_count,
@@ -526,8 +537,6 @@ bsfp_status bsfp_kv_plan(const int32_t* past_lens, const int32_t* q_lens, int32_
                 (int)page_size);
   if (!q_starts || !state || !free_begin)
     return fail(BSFP_ERR_ARG, "%s: null q_starts, state or free_begin", fn);
-  if (state <= free_begin && free_begin < state + 2)
-    return fail(BSFP_ERR_ARG, "%s: state overlaps free_begin", fn);
   if (requests > 0 && (!past_lens || !q_lens || !kv_lens))
     return fail(BSFP_ERR_ARG, "%s: null lengths", fn);
   if (requests > 0 && max_pages > 0 && !block_table)
@@ -535,6 +544,19 @@ bsfp_status bsfp_kv_plan(const int32_t* past_lens, const int32_t* q_lens, int32_
   if (free_count > 0 && !free_pages) return fail(BSFP_ERR_ARG, "%s: null free_pages", fn);
   if (tokens > 0 && (!slots || !positions))
     return fail(BSFP_ERR_ARG, "%s: null slots or positions", fn);
+  // every workgroup reads all lengths and the others write meanwhile
+  const Range written[] = {
+      {"block_table", block_table, (int64_t)requests * max_pages * 4}, {"kv_lens", kv_lens, requests * 4LL},
+      {"q_starts", q_starts, (requests + 1LL) * 4}, {"slots", slots, tokens * 8},
+      {"positions", positions, tokens * 4}, {"state", state, 8}};
+  const Range read[] = {{"past_lens", past_lens, requests * 4LL}, {"q_lens", q_lens, requests * 4LL},
+                        {"free_pages", free_pages, free_count * 4}, {"free_begin", free_begin, 4}};
+  for (const Range& w : written) {
+    for (const Range& r : read)
+      if (overlap(w, r)) return fail(BSFP_ERR_ARG, "%s: %s overlaps %s", fn, w.name, r.name);
+    for (const Range* o = &w + 1; o != std::end(written); ++o)
+      if (overlap(w, *o)) return fail(BSFP_ERR_ARG, "%s: %s overlaps %s", fn, w.name, o->name);
+  }
   return device_status(launch_kv_plan(past_lens, q_lens, requests, page_size, block_table,
                                       max_pages, free_pages, free_count, free_begin, tokens,
                                       kv_lens, q_starts, slots, positions, state,

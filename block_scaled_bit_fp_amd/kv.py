@@ -127,7 +127,8 @@ def kv_plan(past_lens: torch.Tensor, q_lens: torch.Tensor, block_table: torch.Te
     """The step's tables from the request lengths, in one launch (bsfp_kv_plan): new pages from
     free_pages[free_begin:] into block_table (in place), and the kv_lens, q_starts, slots,
     positions and state of the returned KvBatch.  `tokens` bounds the sum of q_lens; rows past
-    the sum get slot and position -1.  out: a KvBatch of earlier outputs to write into."""
+    the sum get slot and position -1.  out: a KvBatch of earlier outputs to write into; they must
+    not be this call's inputs (out.kv_lens is not past_lens: copy it there after the call)."""
     if past_lens.dim() != 1:
         raise ValueError("past_lens must be one-dimensional")
     R = past_lens.shape[0]

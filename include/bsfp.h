@@ -377,12 +377,13 @@ typedef struct {
  * those before it.  A refused request takes no page, its kv_lens is 0 and
  * its slots and positions are -1, so the append skips its rows and its
  * attention rows are empty.  (A negative q counts as 0 in q_starts.)
- *   The inputs are not changed and `state` must not overlap free_begin: the
- * same call again writes the same values.  The caller carries kv_lens over
- * as the next step's past_lens and state[0] as its *free_begin.
+ *   The inputs are not changed, and no output may overlap an input or another
+ * output (kv_lens is not past_lens of the same call): the same call again
+ * writes the same values.  The caller carries kv_lens over as the next step's
+ * past_lens and state[0] as its *free_begin.
  * Errors: BSFP_ERR_ARG for null pointers, requests < 0, max_pages < 0,
- * tokens outside 0 .. 2^31 - 1, free_count outside 0 .. 2^31 - 1, or a page
- * size that is not 16, 32, 64, 128 or 256.
+ * tokens outside 0 .. 2^31 - 1, free_count outside 0 .. 2^31 - 1, a page
+ * size that is not 16, 32, 64, 128 or 256, or buffers that overlap.
  */
 bsfp_status bsfp_kv_plan(const int32_t* past_lens, const int32_t* q_lens, int32_t requests,
                          int32_t page_size, int32_t* block_table, int32_t max_pages,
