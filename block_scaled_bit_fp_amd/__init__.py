@@ -34,9 +34,9 @@ STATUS = {0: "BSFP_OK", 1: "BSFP_ERR_ARG", 2: "BSFP_ERR_UNSUPPORTED", 3: "BSFP_E
 EXPORTS = ("bsfp_amax", "bsfp_quantize", "bsfp_dequantize", "bsfp_qmv", "bsfp_qmv_batch",
            "bsfp_quantize_sr", "bsfp_quantize_ws", "bsfp_qmm_workspace_bytes", "bsfp_qmm",
            "bsfp_qmm_dense_scratch_bytes",
-           "bsfp_qmm_dense", "bsfp_qmm_noalloc", "bsfp_kv_plan", "bsfp_kv_append",
-           "bsfp_kv_attention", "bsfp_kv_attention_workspace_bytes", "bsfp_time_next_launch",
-           "bsfp_last_error", "bsfp_version")
+           "bsfp_qmm_dense", "bsfp_qmm_noalloc", "bsfp_kv_plan", "bsfp_kv_plan_carry",
+           "bsfp_kv_append", "bsfp_kv_attention", "bsfp_kv_attention_workspace_bytes",
+           "bsfp_time_next_launch", "bsfp_last_error", "bsfp_version")
 # most matrices of one bsfp_qmv_batch call (BSFP_QMV_BATCH_MAX)
 QMV_BATCH_MAX = 4
 # bytes of bsfp_quantize_ws's workspace (BSFP_QUANTIZE_WS_BYTES)
@@ -86,6 +86,8 @@ def lib():
             "bsfp_qmm_dense": (C.c_int, [P, I64, QP, P, C.c_size_t, P, P]),
             "bsfp_qmm_noalloc": (C.c_int, [P, I64, QP, I32, P, P]),
             "bsfp_kv_plan": (C.c_int, [P, P, I32, I32, P, I32, P, I64, P, I64, P, P, P, P, P, P]),
+            "bsfp_kv_plan_carry": (C.c_int, [P, P, I32, I32, P, I32, P, I64, P, I64, P, P, P, P, P, P,
+                                             P]),
             "bsfp_kv_append": (C.c_int, [P, I64, P, I64, I64, P, P, P]),
             "bsfp_kv_attention": (C.c_int, [P, I64, I64, I32, P, P, I32, P, P, I32, I32, C.c_float,
                                             I32, P, P, P, C.c_size_t, P]),

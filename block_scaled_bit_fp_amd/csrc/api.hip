@@ -518,13 +518,12 @@ static bool overlap(const Range& a, const Range& b) {
   return a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
 }
 
-bsfp_status bsfp_kv_plan(const int32_t* past_lens, const int32_t* q_lens, int32_t requests,
-                         int32_t page_size, int32_t* block_table, int32_t max_pages,
-                         const int32_t* free_pages, int64_t free_count,
-                         const int32_t* free_begin, int64_t tokens, int32_t* kv_lens,
-                         int32_t* q_starts, int64_t* slots, int32_t* positions, int32_t* state,
-                         bsfp_stream stream) {
-  const char* fn = "bsfp_kv_plan";
+static bsfp_status kv_plan(const char* fn, const int32_t* past_lens, const int32_t* q_lens,
+                           int32_t requests, int32_t page_size, int32_t* block_table,
+                           int32_t max_pages, const int32_t* free_pages, int64_t free_count,
+                           const int32_t* free_begin, int64_t tokens, int32_t* kv_lens,
+                           int32_t* q_starts, int64_t* slots, int32_t* positions, int32_t* state,
+                           int32_t* next_lens, bsfp_stream stream) {
   if (requests < 0 || max_pages < 0)
     return fail(BSFP_ERR_ARG, "%s: negative requests or max_pages", fn);
   if (tokens < 0 || tokens > 0x7fffffffLL)
@@ -548,7 +547,8 @@ bsfp_status bsfp_kv_plan(const int32_t* past_lens, const int32_t* q_lens, int32_
   const Range written[] = {
       {"block_table", block_table, (int64_t)requests * max_pages * 4}, {"kv_lens", kv_lens, requests * 4LL},
       {"q_starts", q_starts, (requests + 1LL) * 4}, {"slots", slots, tokens * 8},
-      {"positions", positions, tokens * 4}, {"state", state, 8}};
+      {"positions", positions, tokens * 4}, {"state", state, 8},
+      {"next_lens", next_lens, next_lens ? requests * 4LL : 0}};
   const Range read[] = {{"past_lens", past_lens, requests * 4LL}, {"q_lens", q_lens, requests * 4LL},
                         {"free_pages", free_pages, free_count * 4}, {"free_begin", free_begin, 4}};
   for (const Range& w : written) {
@@ -559,8 +559,32 @@ bsfp_status bsfp_kv_plan(const int32_t* past_lens, const int32_t* q_lens, int32_
   }
   return device_status(launch_kv_plan(past_lens, q_lens, requests, page_size, block_table,
                                       max_pages, free_pages, free_count, free_begin, tokens,
-                                      kv_lens, q_starts, slots, positions, state,
+                                      kv_lens, q_starts, slots, positions, state, next_lens,
                                       (hipStream_t)stream), fn);
+}
+
+bsfp_status bsfp_kv_plan(const int32_t* past_lens, const int32_t* q_lens, int32_t requests,
+                         int32_t page_size, int32_t* block_table, int32_t max_pages,
+                         const int32_t* free_pages, int64_t free_count,
+                         const int32_t* free_begin, int64_t tokens, int32_t* kv_lens,
+                         int32_t* q_starts, int64_t* slots, int32_t* positions, int32_t* state,
+                         bsfp_stream stream) {
+  return kv_plan("bsfp_kv_plan", past_lens, q_lens, requests, page_size, block_table, max_pages,
+                 free_pages, free_count, free_begin, tokens, kv_lens, q_starts, slots, positions,
+                 state, nullptr, stream);
+}
+
+bsfp_status bsfp_kv_plan_carry(const int32_t* past_lens, const int32_t* q_lens, int32_t requests,
+                               int32_t page_size, int32_t* block_table, int32_t max_pages,
+                               const int32_t* free_pages, int64_t free_count,
+                               const int32_t* free_begin, int64_t tokens, int32_t* kv_lens,
+                               int32_t* q_starts, int64_t* slots, int32_t* positions,
+                               int32_t* state, int32_t* next_lens, bsfp_stream stream) {
+  const char* fn = "bsfp_kv_plan_carry";
+  if (requests > 0 && !next_lens) return fail(BSFP_ERR_ARG, "%s: null next_lens", fn);
+  return kv_plan(fn, past_lens, q_lens, requests, page_size, block_table, max_pages, free_pages,
+                 free_count, free_begin, tokens, kv_lens, q_starts, slots, positions, state,
+                 next_lens, stream);
 }
 
 bsfp_status bsfp_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v,

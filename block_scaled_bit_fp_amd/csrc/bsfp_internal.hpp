@@ -112,7 +112,7 @@ hipError_t launch_kv_plan(const int32_t* past, const int32_t* q, int requests, i
                           int32_t* table, int max_pages, const int32_t* free_pages,
                           int64_t free_count, const int32_t* free_begin, int64_t tokens,
                           int32_t* kv_lens, int32_t* q_starts, int64_t* slots, int32_t* positions,
-                          int32_t* state, hipStream_t s);
+                          int32_t* state, int32_t* next_lens, hipStream_t s);
 hipError_t launch_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v,
                             int64_t v_stride, int64_t tokens, const int64_t* slots,
                             const bsfp_kv_cache& c, hipStream_t s);

@@ -49,7 +49,8 @@ __global__ __launch_bounds__(THREADS) void kv_plan_kernel(
     int page_shift, int32_t* table, int max_pages, const int32_t* __restrict__ free_pages,
     int64_t free_count, const int32_t* __restrict__ free_begin, int64_t tokens,
     int64_t tokens_per_wg, int32_t* __restrict__ kv_lens, int32_t* __restrict__ q_starts,
-    int64_t* __restrict__ slots, int32_t* __restrict__ positions, int32_t* __restrict__ state) {
+    int64_t* __restrict__ slots, int32_t* __restrict__ positions, int32_t* __restrict__ state,
+    int32_t* __restrict__ next_lens) {
   __shared__ int64_t part[THREADS / 64][2];
   __shared__ int64_t s_tot[2];
   __shared__ int64_t s_end[THREADS];      // running sum of q, inclusive
@@ -91,6 +92,7 @@ __global__ __launch_bounds__(THREADS) void kv_plan_kernel(
     }
     if (blockIdx.x == 0 && in) {
       kv_lens[r] = admitted ? past + q : 0;
+      if (next_lens) next_lens[r] = admitted ? past + q : past;
       q_starts[r] = (int32_t)min(end - mine, tokens);
       if (r == requests - 1) q_starts[requests] = (int32_t)min(end, tokens);
       if (admitted && own_need > 0) taken = max(taken, (int32_t)need);
@@ -284,7 +286,7 @@ hipError_t launch_kv_plan(const int32_t* past, const int32_t* q, int requests, i
                           int32_t* table, int max_pages, const int32_t* free_pages,
                           int64_t free_count, const int32_t* free_begin, int64_t tokens,
                           int32_t* kv_lens, int32_t* q_starts, int64_t* slots, int32_t* positions,
-                          int32_t* state, hipStream_t s) {
+                          int32_t* state, int32_t* next_lens, hipStream_t s) {
   // one request per thread: with 256 threads 1021 requests took four rounds of
   // the scan, 10.5 us; up to 256 requests the smaller workgroup starts sooner
   const bool wide = requests > 256;
@@ -295,7 +297,7 @@ hipError_t launch_kv_plan(const int32_t* past, const int32_t* q, int requests, i
     hipLaunchKernelGGL(kernel, dim3((uint32_t)wgs), dim3(threads), 0, s, past, q, requests,
                        __builtin_ctz(page_size), table, max_pages, free_pages, free_count,
                        free_begin, tokens, (tokens + wgs - 1) / wgs, kv_lens, q_starts, slots,
-                       positions, state);
+                       positions, state, next_lens);
   };
   if (wide) go(kv_plan_kernel<1024>, 1024);
   else go(kv_plan_kernel<256>, 256);

@@ -110,6 +110,8 @@ class KvBatch:
     slots: Optional[torch.Tensor] = None       # int64 [tokens]
     positions: Optional[torch.Tensor] = None   # int32 [tokens]
     state: Optional[torch.Tensor] = None       # int32 [2]: next free begin, refused requests
+    # int32 [requests]: the next step's past_lens (kv_lens is 0 for a refused request, this is not)
+    next_lens: Optional[torch.Tensor] = None
 
 
 def _vector(t: torch.Tensor, dtype, shape, what: str) -> torch.Tensor:
@@ -126,9 +128,10 @@ def kv_plan(past_lens: torch.Tensor, q_lens: torch.Tensor, block_table: torch.Te
             page_size: int = 64, out: Optional[KvBatch] = None) -> KvBatch:
     """The step's tables from the request lengths, in one launch (bsfp_kv_plan): new pages from
     free_pages[free_begin:] into block_table (in place), and the kv_lens, q_starts, slots,
-    positions and state of the returned KvBatch.  `tokens` bounds the sum of q_lens; rows past
-    the sum get slot and position -1.  out: a KvBatch of earlier outputs to write into; they must
-    not be this call's inputs (out.kv_lens is not past_lens: copy it there after the call)."""
+    positions, state and next_lens of the returned KvBatch.  `tokens` bounds the sum of q_lens;
+    rows past the sum get slot and position -1.  The next step's past_lens is next_lens, its
+    free_begin state[:1].  out: a KvBatch of earlier outputs to write into; they must not be this
+    call's inputs (out.next_lens is not past_lens: copy it there after the call)."""
     if past_lens.dim() != 1:
         raise ValueError("past_lens must be one-dimensional")
     R = past_lens.shape[0]
@@ -143,10 +146,10 @@ def kv_plan(past_lens: torch.Tensor, q_lens: torch.Tensor, block_table: torch.Te
     if tokens < 0:
         raise ValueError("tokens must not be negative")
     if out is None:
-        lens, starts, positions, state = torch.split_with_sizes(
-            past_lens.new_empty(2 * R + tokens + 3), (R, R + 1, tokens, 2))
+        lens, starts, positions, state, after = torch.split_with_sizes(
+            past_lens.new_empty(3 * R + tokens + 3), (R, R + 1, tokens, 2, R))
         out = KvBatch(block_table, lens, starts, past_lens.new_empty(tokens, dtype=torch.int64),
-                      positions, state)
+                      positions, state, after)
     else:
         if out.block_table is not block_table:
             raise ValueError("out belongs to another block_table")
@@ -155,12 +158,16 @@ def kv_plan(past_lens: torch.Tensor, q_lens: torch.Tensor, block_table: torch.Te
         _vector(out.slots, torch.int64, (tokens,), "out.slots")
         _vector(out.positions, i32, (tokens,), "out.positions")
         _vector(out.state, i32, (2,), "out.state")
-    _check(lib().bsfp_kv_plan(past_lens.data_ptr(), q_lens.data_ptr(), R, page_size,
-                              block_table.data_ptr(), block_table.shape[1],
-                              free_pages.data_ptr(), free_pages.numel(), free_begin.data_ptr(),
-                              tokens, out.kv_lens.data_ptr(), out.q_starts.data_ptr(),
-                              out.slots.data_ptr(), out.positions.data_ptr(),
-                              out.state.data_ptr(), _stream()))
+        if out.next_lens is None:
+            out.next_lens = past_lens.new_empty(R)
+        _vector(out.next_lens, i32, (R,), "out.next_lens")
+    _check(lib().bsfp_kv_plan_carry(past_lens.data_ptr(), q_lens.data_ptr(), R, page_size,
+                                    block_table.data_ptr(), block_table.shape[1],
+                                    free_pages.data_ptr(), free_pages.numel(),
+                                    free_begin.data_ptr(), tokens, out.kv_lens.data_ptr(),
+                                    out.q_starts.data_ptr(), out.slots.data_ptr(),
+                                    out.positions.data_ptr(), out.state.data_ptr(),
+                                    out.next_lens.data_ptr(), _stream()))
     return out
 
 

@@ -70,7 +70,7 @@ class Block:
         o = o.view(T, self.heads * D)
         y = x + (bs.qmv(o, self.wo) if T <= 8 else bs.qmm(o, self.wo))
         # the step's lengths and free pages are the next one's
-        self.lens.copy_(batch.kv_lens)
+        self.lens.copy_(batch.next_lens)
         self.begin.copy_(batch.state[:1])
         return y, batch, o
 

@@ -376,11 +376,14 @@ typedef struct {
  * `tokens`, or the free list does not hold the pages of this request and of
  * those before it.  A refused request takes no page, its kv_lens is 0 and
  * its slots and positions are -1, so the append skips its rows and its
- * attention rows are empty.  (A negative q counts as 0 in q_starts.)
+ * attention rows are empty; what it has in the cache stays.  (A negative q
+ * counts as 0 in q_starts.)
  *   The inputs are not changed, and no output may overlap an input or another
  * output (kv_lens is not past_lens of the same call): the same call again
- * writes the same values.  The caller carries kv_lens over as the next step's
- * past_lens and state[0] as its *free_begin.
+ * writes the same values.  The caller carries state[0] over as the next step's
+ * *free_begin and, as its past_lens, what each request then has in the cache:
+ * kv_lens, but past_lens where the request was refused.  bsfp_kv_plan_carry
+ * writes that too.
  * Errors: BSFP_ERR_ARG for null pointers, requests < 0, max_pages < 0,
  * tokens outside 0 .. 2^31 - 1, free_count outside 0 .. 2^31 - 1, a page
  * size that is not 16, 32, 64, 128 or 256, or buffers that overlap.
@@ -391,6 +394,19 @@ bsfp_status bsfp_kv_plan(const int32_t* past_lens, const int32_t* q_lens, int32_
                          const int32_t* free_begin, int64_t tokens, int32_t* kv_lens,
                          int32_t* q_starts, int64_t* slots, int32_t* positions, int32_t* state,
                          bsfp_stream stream);
+
+/*
+ * bsfp_kv_plan_carry: bsfp_kv_plan with one output more, next_lens [requests]:
+ * past + q of an admitted request and past, as given, of a refused one.  It is
+ * the next step's past_lens, so a refused request goes on where it stood once
+ * there are pages for it.  Errors: those of bsfp_kv_plan.
+ */
+bsfp_status bsfp_kv_plan_carry(const int32_t* past_lens, const int32_t* q_lens, int32_t requests,
+                               int32_t page_size, int32_t* block_table, int32_t max_pages,
+                               const int32_t* free_pages, int64_t free_count,
+                               const int32_t* free_begin, int64_t tokens, int32_t* kv_lens,
+                               int32_t* q_starts, int64_t* slots, int32_t* positions,
+                               int32_t* state, int32_t* next_lens, bsfp_stream stream);
 
 /*
  * bsfp_kv_append: quantizes the rows k, v [tokens, kv_heads, head_dim] (bf16;
