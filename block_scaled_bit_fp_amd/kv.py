@@ -71,13 +71,15 @@ class KvCache:
         return self.k.codes.device
 
     def desc(self):
-        """The C descriptor, by reference; rebuilt when a tensor's descriptor is."""
+        """The C descriptor, by reference; rebuilt when a field or a tensor's descriptor changed."""
         kd, vd = self.k.desc(), self.v.desc()
+        heads, page = self.kv_heads, self.page_size
         cached = self.__dict__.get("_kv_desc")
-        if cached is None or cached[0] is not kd or cached[1] is not vd:
-            d = KvCacheDesc(C.pointer(kd), C.pointer(vd), self.pages, self.kv_heads, self.page_size)
-            self.__dict__["_kv_desc"] = cached = (kd, vd, C.byref(d), d)
-        return cached[2]
+        if (cached is None or cached[0] is not kd or cached[1] is not vd or cached[2] != heads
+                or cached[3] != page):
+            d = KvCacheDesc(C.pointer(kd), C.pointer(vd), self.pages, heads, page)
+            self.__dict__["_kv_desc"] = cached = (kd, vd, heads, page, C.byref(d))
+        return cached[4]
 
 
 def empty_kv_cache(mode: int, pages: int, kv_heads: int, head_dim: int, page_size: int = 64,

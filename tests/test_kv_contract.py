@@ -44,3 +44,23 @@ def test_plan_refuses_buffers_that_overlap(b, out, other):
 def test_plan_names_the_null_buffer(b, name):
     status, message = plan(b, **{name: None})
     assert status == ARG and "null" in message
+
+
+def test_cache_descriptor_follows_its_fields(b):
+    c = b.empty_kv_cache(b.MXFP4, 4, 2, 64, page_size=32, device="cpu")
+
+    def fields():
+        d = c.desc()._obj
+        return d.pages, d.kv_heads, d.page_size, d.k.contents.codes, d.v.contents.codes
+    at = c.k.codes.data_ptr(), c.v.codes.data_ptr()
+    assert fields() == (4, 2, 32, *at)
+    kept = c.desc()
+    assert c.desc() is kept  # rebuilt only when something changed
+    c.page_size = 64
+    assert fields() == (2, 2, 64, *at)
+    c.kv_heads = 1
+    assert fields() == (4, 1, 64, *at)
+    c.k.codes = c.k.codes.clone()
+    assert fields() == (4, 1, 64, c.k.codes.data_ptr(), at[1])
+    c.v = b.empty_quantized(b.MXFP4, c.k.rows, 64, "cpu")
+    assert fields() == (4, 1, 64, c.k.codes.data_ptr(), c.v.codes.data_ptr())
