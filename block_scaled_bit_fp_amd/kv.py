@@ -46,9 +46,13 @@ class KvCache:
                              f"{self.page_size} tokens")
         if (self.k.mode, self.k.rows, self.k.cols) != (self.v.mode, self.v.rows, self.v.cols):
             raise ValueError("K and V differ in format or shape")
-        if self.k.codes.device != self.v.codes.device:
-            raise ValueError("K and V are on different devices")
         for t in (self.k, self.v):
+            g = t.global_scale
+            if g is not None and (g.dtype != torch.float32 or g.numel() != 1):
+                raise ValueError("a global scale is one fp32 value")
+            for buf in (t.codes, t.scales, t.biases, g):
+                if buf is not None and buf.device != self.device:
+                    raise ValueError(f"the cache's tensors are on {self.device} and {buf.device}")
             G, words = t.group_size, t.cols * t.nbits // 32
             want = [(t.codes, t.rows * words * 4), (t.scales, t.rows * (t.cols // G) *
                                                     (2 if t.mode == AFFINE else 1))]
@@ -77,6 +81,7 @@ class KvCache:
         cached = self.__dict__.get("_kv_desc")
         if (cached is None or cached[0] is not kd or cached[1] is not vd or cached[2] != heads
                 or cached[3] != page):
+            self.__post_init__()
             d = KvCacheDesc(C.pointer(kd), C.pointer(vd), self.pages, heads, page)
             self.__dict__["_kv_desc"] = cached = (kd, vd, heads, page, C.byref(d))
         return cached[4]
@@ -116,12 +121,12 @@ class KvBatch:
     next_lens: Optional[torch.Tensor] = None
 
 
-def _vector(t: torch.Tensor, dtype, shape, what: str) -> torch.Tensor:
+def _vector(t: torch.Tensor, dtype, shape, what: str, device) -> torch.Tensor:
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous tensor on the GPU")
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous tensor on the call's GPU ({device})")
     return t
 
 
@@ -136,15 +141,15 @@ def kv_plan(past_lens: torch.Tensor, q_lens: torch.Tensor, block_table: torch.Te
     call's inputs (out.next_lens is not past_lens: copy it there after the call)."""
     if past_lens.dim() != 1:
         raise ValueError("past_lens must be one-dimensional")
-    R = past_lens.shape[0]
+    R, device = past_lens.shape[0], past_lens.device
     i32 = torch.int32
-    _vector(past_lens, i32, (R,), "past_lens")
-    _vector(q_lens, i32, (R,), "q_lens")
+    _vector(past_lens, i32, (R,), "past_lens", device)
+    _vector(q_lens, i32, (R,), "q_lens", device)
     if block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError(f"block_table must have {R} rows")
-    _vector(block_table, i32, block_table.shape, "block_table")
-    _vector(free_pages, i32, (free_pages.numel(),), "free_pages")
-    _vector(free_begin, i32, (1,), "free_begin")
+    _vector(block_table, i32, block_table.shape, "block_table", device)
+    _vector(free_pages, i32, (free_pages.numel(),), "free_pages", device)
+    _vector(free_begin, i32, (1,), "free_begin", device)
     if tokens < 0:
         raise ValueError("tokens must not be negative")
     if out is None:
@@ -155,14 +160,14 @@ def kv_plan(past_lens: torch.Tensor, q_lens: torch.Tensor, block_table: torch.Te
     else:
         if out.block_table is not block_table:
             raise ValueError("out belongs to another block_table")
-        _vector(out.kv_lens, i32, (R,), "out.kv_lens")
-        _vector(out.q_starts, i32, (R + 1,), "out.q_starts")
-        _vector(out.slots, torch.int64, (tokens,), "out.slots")
-        _vector(out.positions, i32, (tokens,), "out.positions")
-        _vector(out.state, i32, (2,), "out.state")
+        _vector(out.kv_lens, i32, (R,), "out.kv_lens", device)
+        _vector(out.q_starts, i32, (R + 1,), "out.q_starts", device)
+        _vector(out.slots, torch.int64, (tokens,), "out.slots", device)
+        _vector(out.positions, i32, (tokens,), "out.positions", device)
+        _vector(out.state, i32, (2,), "out.state", device)
         if out.next_lens is None:
             out.next_lens = past_lens.new_empty(R)
-        _vector(out.next_lens, i32, (R,), "out.next_lens")
+        _vector(out.next_lens, i32, (R,), "out.next_lens", device)
     _check(lib().bsfp_kv_plan_carry(past_lens.data_ptr(), q_lens.data_ptr(), R, page_size,
                                     block_table.data_ptr(), block_table.shape[1],
                                     free_pages.data_ptr(), free_pages.numel(),
@@ -173,14 +178,16 @@ def kv_plan(past_lens: torch.Tensor, q_lens: torch.Tensor, block_table: torch.Te
     return out
 
 
-def _rows(t: torch.Tensor, heads: Optional[int], head_dim: int, what: str) -> int:
+def _rows(t: torch.Tensor, heads: Optional[int], cache: KvCache, what: str) -> int:
     """Checks bf16 rows [tokens, heads, head_dim] with contiguous heads and columns; returns the
     token stride in elements."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{what}: expected bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise TypeError(f"{what}: expected a tensor on the GPU")
-    shape = t.shape
+    if t.device != cache.device:
+        raise ValueError(f"{what} is on {t.device}, the cache on {cache.device}")
+    shape, head_dim = t.shape, cache.head_dim
     if len(shape) != 3 or shape[2] != head_dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{what} must be [tokens, {'heads' if heads is None else heads}, "
                          f"{head_dim}], got {tuple(shape)}")
@@ -194,11 +201,11 @@ def kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     """Quantizes the rows k, v [tokens, kv_heads, head_dim] into the cache at `slots`
     (bsfp_kv_append); rows whose slot is negative are skipped.  k and v may be columns of one
     fused projection's output (any token stride that is a multiple of 8)."""
-    ks = _rows(k, cache.kv_heads, cache.head_dim, "k")
-    vs = _rows(v, cache.kv_heads, cache.head_dim, "v")
+    ks = _rows(k, cache.kv_heads, cache, "k")
+    vs = _rows(v, cache.kv_heads, cache, "v")
     if v.shape[0] != k.shape[0]:
         raise ValueError(f"k has {k.shape[0]} rows, v has {v.shape[0]}")
-    _vector(slots, torch.int64, (k.shape[0],), "slots")
+    _vector(slots, torch.int64, (k.shape[0],), "slots", k.device)
     _check(lib().bsfp_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0], slots.data_ptr(),
                                 cache.desc(), _stream()))
 
@@ -223,25 +230,26 @@ def kv_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: Optiona
     (bsfp_kv_attention).  scale: 1/sqrt(head_dim) by default; window > 0: only that many keys
     up to the row's own; max_q: an upper bound on the batch's q_lens if the host knows one (1 in
     a decode step).  Returns out, or (out, lse) with return_lse."""
-    stride = _rows(q, None, cache.head_dim, "q")
+    stride = _rows(q, None, cache, "q")
     T, H, D = q.shape
+    device = q.device
     table, lens, starts = batch.block_table, batch.kv_lens, batch.q_starts
     R, M = table.shape
-    _vector(table, torch.int32, (R, M), "block_table")
-    _vector(lens, torch.int32, (R,), "kv_lens")
-    _vector(starts, torch.int32, (R + 1,), "q_starts")
+    _vector(table, torch.int32, (R, M), "block_table", device)
+    _vector(lens, torch.int32, (R,), "kv_lens", device)
+    _vector(starts, torch.int32, (R + 1,), "q_starts", device)
     if out is None:
         out = q.new_empty((T, H, D))
     else:
-        _vector(out, torch.bfloat16, (T, H, D), "out")
+        _vector(out, torch.bfloat16, (T, H, D), "out", device)
     if lse is not None:
-        _vector(lse, torch.float32, (T, H), "lse")
+        _vector(lse, torch.float32, (T, H), "lse", device)
     elif return_lse:
         lse = q.new_empty((T, H), dtype=torch.float32)
     if workspace is None:
         workspace = kv_attention_workspace(T, H, cache, R)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the GPU")
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
     _check(lib().bsfp_kv_attention(
         q.data_ptr(), stride, T, H, cache.desc(), table.data_ptr(), M, lens.data_ptr(),
         starts.data_ptr(), R, max(T, 1) if max_q is None else max_q,

@@ -64,3 +64,106 @@ def test_cache_descriptor_follows_its_fields(b):
     assert fields() == (4, 1, 64, c.k.codes.data_ptr(), at[1])
     c.v = b.empty_quantized(b.MXFP4, c.k.rows, 64, "cpu")
     assert fields() == (4, 1, 64, c.k.codes.data_ptr(), c.v.codes.data_ptr())
+
+
+class Fake:
+    """A tensor that is nowhere, named to stand on a device; its pointer must never be asked for."""
+
+    def __init__(self, shape, dtype=torch.int32, device="cuda:0"):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
+        self.is_cuda = self.device.type == "cuda"
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def stride(self):
+        n = [1]
+        for s in reversed(self.shape[1:]):
+            n.insert(0, n[0] * s)
+        return tuple(n)
+
+    def is_contiguous(self):
+        return True
+
+    def new_empty(self, shape, dtype=None):
+        return Fake((shape,) if isinstance(shape, int) else shape, dtype or self.dtype, self.device)
+
+    def data_ptr(self):
+        raise AssertionError("the call was not refused")
+
+
+BF16 = torch.bfloat16
+
+
+def fake_cache(b, device="cuda:0"):
+    def side():
+        return b.QuantizedTensor(b.MXFP4, 64, 64, Fake((64, 8), device=device), Fake((64, 2), torch.uint8, device))
+    return b.KvCache(side(), side(), kv_heads=2, page_size=16)
+
+
+def attention_call(b, **change):
+    a = dict(q=Fake((3, 4, 64), BF16), table=Fake((2, 5)), lens=Fake((2,)), starts=Fake((3,)), cache=fake_cache(b),
+             out=Fake((3, 4, 64), BF16), lse=Fake((3, 4), torch.float32), workspace=Fake((1 << 28,), torch.uint8))
+    a.update(change)
+    return b.kv_attention(a["q"], a["cache"], b.KvBatch(a["table"], a["lens"], a["starts"]), out=a["out"], lse=a["lse"],
+                          workspace=a["workspace"])
+
+
+@pytest.mark.parametrize("name,shape,dtype", [
+    ("q", (3, 4, 64), BF16), ("table", (2, 5), torch.int32), ("lens", (2,), torch.int32), ("starts", (3,), torch.int32),
+    ("out", (3, 4, 64), BF16), ("lse", (3, 4), torch.float32), ("workspace", (1 << 28,), torch.uint8)])
+def test_attention_refuses_tensors_of_another_device(b, name, shape, dtype):
+    with pytest.raises(ValueError, match="cuda"):
+        attention_call(b, **{name: Fake(shape, dtype, "cuda:1")})
+
+
+@pytest.mark.parametrize("device", ["cpu", "cuda:1"])
+def test_calls_refuse_a_cache_of_another_device(b, device):
+    with pytest.raises(ValueError, match=device):
+        attention_call(b, cache=fake_cache(b, device))
+    k = Fake((3, 2, 64), BF16)
+    with pytest.raises(ValueError, match=device):
+        b.kv_append(fake_cache(b, device), k, k, Fake((3,), torch.int64))
+
+
+@pytest.mark.parametrize("bad", ["k", "v", "slots"])
+def test_append_refuses_tensors_of_another_device(b, bad):
+    a = {n: Fake((3, 2, 64), BF16, "cuda:1" if n == bad else "cuda:0") for n in ("k", "v")}
+    slots = Fake((3,), torch.int64, "cuda:1" if bad == "slots" else "cuda:0")
+    with pytest.raises(ValueError, match="cuda"):
+        b.kv_append(fake_cache(b), a["k"], a["v"], slots)
+
+
+@pytest.mark.parametrize("bad", range(10))
+def test_plan_refuses_tensors_of_another_device(b, bad):
+    shapes = [(2,), (2,), (2, 5), (7,), (1,)]
+    dev = ["cuda:1" if i == bad else "cuda:0" for i in range(10)]
+    a = [Fake(s, device=d) for s, d in zip(shapes, dev)]
+    out = b.KvBatch(a[2], Fake((2,), device=dev[5]), Fake((3,), device=dev[6]), Fake((4,), torch.int64, dev[7]),
+                    Fake((4,), device=dev[8]), Fake((2,), device=dev[9]), Fake((2,)))
+    with pytest.raises(ValueError, match="cuda"):
+        b.kv_plan(*a, tokens=4, page_size=16, out=out)
+
+
+def test_cache_refuses_parts_that_do_not_belong_together(b):
+    def cache(**change):
+        c = b.empty_kv_cache(b.NVFP4, 4, 2, 64, page_size=16, device="cpu")
+        for name, t in change.items():
+            setattr(c.v, name, t)
+        return c
+    for change in (dict(scales=torch.empty((128, 4), dtype=torch.uint8, device="meta")),
+                   dict(codes=torch.empty((128, 8), dtype=torch.int32, device="meta")),
+                   dict(global_scale=torch.empty(1, device="meta")), dict(global_scale=torch.empty(1, dtype=torch.float64)),
+                   dict(global_scale=torch.empty(2)), dict(scales=torch.empty((64, 4), dtype=torch.uint8))):
+        c = cache(**change)
+        with pytest.raises(ValueError):
+            b.KvCache(c.k, c.v, kv_heads=2, page_size=16)
+        with pytest.raises(ValueError):  # and of a cache whose parts were exchanged
+            c.desc()
+    assert cache(global_scale=torch.empty(1)).desc()
