@@ -682,7 +682,7 @@ template <int MODE, int D>
 hipError_t run(const KvParams& p, void* ws, hipStream_t s) {
   JoinSide split = {{}, std::min(device_cu_count() * wgs_per_cu(MODE, D), kMaxRuns), kRows};
   split.parts = kv_parts(ws, split.runs, kRows, D);
-  launch_main(kv_split_kernel<MODE, D>, dim3(split.runs), dim3(kThreads), 0, s, p, split.parts);
+  hipLaunchKernelGGL((kv_split_kernel<MODE, D>), dim3(split.runs), dim3(kThreads), 0, s, p, split.parts);
   hipError_t e = hipGetLastError();
   int live = (int)std::min<int64_t>((int64_t)p.max_q * p.group, kRows);
   // the longest segment there can be; none is cut up to kWhole tiles

@@ -674,8 +674,8 @@ int prompt_runs(int mode, int D) {
 template <int MODE, int D>
 hipError_t run(const KvParams& p, void* ws, int* runs, bool* join, hipStream_t s) {
   *runs = prompt_runs(MODE, D);
-  launch_main(kv_prompt_kernel<MODE, D>, dim3(*runs), dim3(kThreads), 0, s, p,
-              kv_parts(ws, *runs, kBlock, D));
+  hipLaunchKernelGGL((kv_prompt_kernel<MODE, D>), dim3(*runs), dim3(kThreads), 0, s, p,
+                     kv_parts(ws, *runs, kBlock, D));
   // the longest segment there can be; none is cut up to kWhole tiles
   int64_t keys = (int64_t)p.max_pages << p.page_shift;
   if (p.window)

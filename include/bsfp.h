@@ -474,7 +474,8 @@ size_t bsfp_kv_attention_workspace_bytes(int64_t tokens, int32_t heads, int32_t 
  * commands queued between kernels.  start_event and stop_event are hipEvent_t
  * handles the caller created (timing enabled) and still owns; either may be
  * NULL.  One-shot: the pair is cleared by the launch that uses it, and
- * passing two NULLs clears a pending pair.  Always returns BSFP_OK.
+ * passing two NULLs clears a pending pair; calls of other functions in between
+ * leave it pending.  Always returns BSFP_OK.
  */
 bsfp_status bsfp_time_next_launch(void* start_event, void* stop_event);
 
