@@ -632,8 +632,9 @@ bsfp_status bsfp_kv_attention(const uint16_t* q, int64_t q_stride, int64_t token
                 (int)heads, (int)cache->kv_heads);
   if (max_q < 1) return fail(BSFP_ERR_ARG, "%s: max_q = %d below 1", fn, (int)max_q);
   if (window < 0) return fail(BSFP_ERR_ARG, "%s: negative window", fn);
-  if (!(scale > 0.0f) || scale > 3.0e38f)
-    return fail(BSFP_ERR_ARG, "%s: scale must be positive and finite", fn);
+  // the kernels take exponentials to base 2
+  if (!(scale > 0.0f) || !(scale * 1.4426950408889634f <= 3.402823466e38f))
+    return fail(BSFP_ERR_ARG, "%s: scale must be positive, and finite times log2 e", fn);
   if (tokens == 0) return ok();
   if (tokens > 0x7fffffffLL / heads)
     return fail(BSFP_ERR_UNSUPPORTED, "%s: %lld tokens x %d heads exceed 2^31 - 1 rows", fn,

@@ -446,8 +446,8 @@ bsfp_status bsfp_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* 
  *   separate ones
  * Products run on the matrix cores with fp32 sums; maxima, sums and lse are
  * fp32.  Results are the same on every call (no atomics).
- * Errors: BSFP_ERR_ARG for bad pointers, shapes, strides, max_q < 1 or a
- * small workspace; BSFP_ERR_UNSUPPORTED for formats or head dimensions
+ * Errors: BSFP_ERR_ARG for bad pointers, shapes, strides, max_q < 1, a scale
+ * that is not positive or not finite times log2 e, or a small workspace; BSFP_ERR_UNSUPPORTED for formats or head dimensions
  * outside the above, heads not a multiple of kv_heads, or more than 2^31 - 1
  * rows.
  */

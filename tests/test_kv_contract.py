@@ -167,3 +167,19 @@ def test_cache_refuses_parts_that_do_not_belong_together(b):
         with pytest.raises(ValueError):  # and of a cache whose parts were exchanged
             c.desc()
     assert cache(global_scale=torch.empty(1)).desc()
+
+
+def attend(b, max_pages=2, scale=1.0):
+    """bsfp_kv_attention over two requests at addresses that are never dereferenced."""
+    from block_scaled_bit_fp_amd.kv import KvCacheDesc
+    at = 0x10000
+    k, v = (b.QTensorDesc(b.MXFP4, 4, 32, 4 * 2 * 16, 64, at, at, None, None, None) for _ in range(2))
+    c = KvCacheDesc(C.pointer(k), C.pointer(v), 4, 2, 16)
+    return b.lib().bsfp_kv_attention(at, 256, 3, 4, C.byref(c), at, max_pages, at, at, 2, 1, scale, 0, at, None, at,
+                                     1 << 40, None)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3e38])
+def test_attention_refuses_a_scale_that_overflows_in_log2_units(b, scale):
+    assert attend(b, scale=scale) == ARG
+    assert "scale" in b.lib().bsfp_last_error().decode()
