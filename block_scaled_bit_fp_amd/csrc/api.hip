@@ -627,6 +627,9 @@ bsfp_status bsfp_kv_attention(const uint16_t* q, int64_t q_stride, int64_t token
   if (st != BSFP_OK) return st;
   if (tokens < 0 || requests < 0 || max_pages < 0)
     return fail(BSFP_ERR_ARG, "%s: negative tokens, requests or max_pages", fn);
+  if ((int64_t)max_pages * cache->page_size > kKvMaxKeys)
+    return fail(BSFP_ERR_UNSUPPORTED, "%s: a table of %d pages x %d tokens exceeds %lld keys", fn,
+                (int)max_pages, (int)cache->page_size, (long long)kKvMaxKeys);
   if (heads < 1 || heads % cache->kv_heads)
     return fail(BSFP_ERR_UNSUPPORTED, "%s: %d heads are not a multiple of %d kv heads", fn,
                 (int)heads, (int)cache->kv_heads);

@@ -117,6 +117,10 @@ hipError_t launch_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t*
                             int64_t v_stride, int64_t tokens, const int64_t* slots,
                             const bsfp_kv_cache& c, hipStream_t s);
 
+// Keys that a request's table may hold: key numbers are 32-bit, and the loads
+// and masks of the attention kernels run up to 16 tiles of 64 past the last.
+constexpr int64_t kKvMaxKeys = (int64_t(1) << 31) - 8192;
+
 struct KvAttentionArgs {
   const uint16_t* q;
   int64_t q_stride, tokens;

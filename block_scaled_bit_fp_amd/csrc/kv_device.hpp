@@ -336,7 +336,7 @@ __device__ __forceinline__ KvRequest kv_request(const KvParams& p, int row0, int
   q.row0 = row0;
   q.q_len = q_len;
   q.kv = kv;
-  q.last = (int)min((int64_t)p.max_pages << p.page_shift, (int64_t)0x7fffff00);
+  q.last = p.max_pages << p.page_shift;  // at most kKvMaxKeys
   q.end = q.q_len ? min(q.kv, q.last) : 0;
   q.first = p.window ? (int)max((int64_t)q.kv - q.q_len - p.window + 1, (int64_t)0) : 0;
   q.first = min(q.first, q.end);

@@ -448,8 +448,8 @@ bsfp_status bsfp_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* 
  * fp32.  Results are the same on every call (no atomics).
  * Errors: BSFP_ERR_ARG for bad pointers, shapes, strides, max_q < 1, a scale
  * that is not positive or not finite times log2 e, or a small workspace; BSFP_ERR_UNSUPPORTED for formats or head dimensions
- * outside the above, heads not a multiple of kv_heads, or more than 2^31 - 1
- * rows.
+ * outside the above, heads not a multiple of kv_heads, more than 2^31 - 1
+ * rows, or a table of more than 2^31 - 8192 keys (max_pages * page_size).
  */
 bsfp_status bsfp_kv_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int32_t heads,
                               const bsfp_kv_cache* cache, const int32_t* block_table,

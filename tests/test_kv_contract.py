@@ -183,3 +183,10 @@ def attend(b, max_pages=2, scale=1.0):
 def test_attention_refuses_a_scale_that_overflows_in_log2_units(b, scale):
     assert attend(b, scale=scale) == ARG
     assert "scale" in b.lib().bsfp_last_error().decode()
+
+
+def test_attention_refuses_tables_whose_keys_pass_31_bits(b):
+    """Key numbers are 32-bit and run a few tiles past the last one."""
+    for max_pages in ((1 << 27) - 511, 1 << 27, (1 << 31) - 1):
+        assert attend(b, max_pages=max_pages) == UNSUPPORTED
+        assert "keys" in b.lib().bsfp_last_error().decode()
