@@ -178,6 +178,11 @@ def kv_plan(past_lens: torch.Tensor, q_lens: torch.Tensor, block_table: torch.Te
     return out
 
 
+def _int32(n: int) -> int:
+    """A bound on lengths, which are 32-bit: no larger one says more (ctypes would wrap it)."""
+    return min(max(n, -1), 0x7fffffff)
+
+
 def _rows(t: torch.Tensor, heads: Optional[int], cache: KvCache, what: str) -> int:
     """Checks bf16 rows [tokens, heads, head_dim] with contiguous heads and columns; returns the
     token stride in elements."""
@@ -252,8 +257,8 @@ def kv_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: Optiona
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     _check(lib().bsfp_kv_attention(
         q.data_ptr(), stride, T, H, cache.desc(), table.data_ptr(), M, lens.data_ptr(),
-        starts.data_ptr(), R, max(T, 1) if max_q is None else max_q,
-        1.0 / math.sqrt(D) if scale is None else scale, window, out.data_ptr(),
+        starts.data_ptr(), R, max(T, 1) if max_q is None else _int32(max_q),
+        1.0 / math.sqrt(D) if scale is None else scale, _int32(window), out.data_ptr(),
         None if lse is None else lse.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream()))
     return (out, lse) if return_lse else out

@@ -121,3 +121,16 @@ def test_values_near_the_end_of_the_range(bsfp, mode, kv, q_lens):
         v = (rand((n, 2, 128), 50 + r).float().clamp(-4, 4) * 2.0 ** 115).to(torch.bfloat16)
         bsfp.kv_append(cache, rand((n, 2, 128), 60 + r), v, slots)
     check_attention(bsfp, cache, batch, q)
+
+
+def test_window_and_max_q_beyond_32_bits(bsfp):
+    """No request is that long: as without a window, and as without a bound."""
+    cache, batch, q = build(bsfp, NVFP4, [100, 80], [1, 30], 4, 1, 64, 16, seed=8)
+    want = bsfp.kv_attention(q, cache, batch)
+    for big in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63):
+        assert torch.equal(bsfp.kv_attention(q, cache, batch, window=big), want), big
+        assert torch.equal(bsfp.kv_attention(q, cache, batch, max_q=big + 1), want), big
+    for bad in (dict(window=-2 ** 32), dict(max_q=-2 ** 32 + 1)):
+        with pytest.raises(bsfp.BsfpError) as ei:
+            bsfp.kv_attention(q, cache, batch, **bad)
+        assert ei.value.status == 1
