@@ -160,10 +160,11 @@ class QuantizedTensor:
 
     def desc(self) -> QTensorDesc:
         """The C descriptor; rebuilt whenever a field or a tensor's storage changed."""
-        b, g, a = self.biases, self.global_scale, self.amax
-        key = (self.mode, self.bits, self.group, self.rows, self.cols, self.codes.data_ptr(),
-               self.scales.data_ptr(), None if b is None else b.data_ptr(),
-               None if g is None else g.data_ptr(), None if a is None else a.data_ptr())
+        c, s, b, g, a = self.codes, self.scales, self.biases, self.global_scale, self.amax
+        key = (self.mode, self.bits, self.group, self.rows, self.cols,
+               None if c is None else c.data_ptr(), None if s is None else s.data_ptr(),
+               None if b is None else b.data_ptr(), None if g is None else g.data_ptr(),
+               None if a is None else a.data_ptr())
         cached = self.__dict__.get("_desc")
         if cached is None or cached[0] != key:
             d = QTensorDesc(self.mode, self.nbits, self.group_size, *key[3:])
