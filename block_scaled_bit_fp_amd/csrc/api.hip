@@ -8,6 +8,7 @@
 // load-time convert-or-reject policy", Gate impact).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <iterator>
@@ -652,8 +653,8 @@ bsfp_status bsfp_kv_attention(const uint16_t* q, int64_t q_stride, int64_t token
     return fail(BSFP_ERR_ARG, "%s: null q_starts or kv_lens", fn);
   if (requests > 0 && max_pages > 0 && !block_table)
     return fail(BSFP_ERR_ARG, "%s: null block_table", fn);
-  const size_t need = kv_attention_workspace(tokens, heads, cache->kv_heads, (int)cache->k->cols,
-                                             requests);
+  const size_t need = kv_attention_workspace(std::min<int64_t>(tokens, max_q), heads, cache->kv_heads,
+                                             (int)cache->k->cols, requests);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return fail(BSFP_ERR_ARG, "%s: workspace needs %zu bytes (16-byte aligned), got %zu", fn, need,
                 workspace_bytes);

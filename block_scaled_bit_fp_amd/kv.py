@@ -220,9 +220,12 @@ def kv_attention_workspace_bytes(tokens: int, heads: int, kv_heads: int, head_di
     return int(lib().bsfp_kv_attention_workspace_bytes(tokens, heads, kv_heads, head_dim, requests))
 
 
-def kv_attention_workspace(tokens: int, heads: int, cache: KvCache, requests: int) -> torch.Tensor:
-    """A workspace for kv_attention calls of at most these sizes, to keep between calls."""
-    need = kv_attention_workspace_bytes(tokens, heads, cache.kv_heads, cache.head_dim, requests)
+def kv_attention_workspace(tokens: int, heads: int, cache: KvCache, requests: int,
+                           max_q: Optional[int] = None) -> torch.Tensor:
+    """A workspace for kv_attention calls of at most these sizes, to keep between calls.  With
+    max_q it is for calls that give no larger one (a decode step's is far smaller)."""
+    rows = tokens if max_q is None else min(tokens, max_q)
+    need = kv_attention_workspace_bytes(rows, heads, cache.kv_heads, cache.head_dim, requests)
     return torch.empty(need, dtype=torch.uint8, device=cache.device)
 
 
@@ -252,7 +255,7 @@ def kv_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: Optiona
     elif return_lse:
         lse = q.new_empty((T, H), dtype=torch.float32)
     if workspace is None:
-        workspace = kv_attention_workspace(T, H, cache, R)
+        workspace = kv_attention_workspace(T, H, cache, R, max_q)
     elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     _check(lib().bsfp_kv_attention(

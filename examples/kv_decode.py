@@ -79,8 +79,8 @@ class Block:
         f = x.float()
         return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + 1e-6)).to(torch.bfloat16)
 
-    def workspace(self, tokens):
-        return bs.kv_attention_workspace(tokens, self.heads, self.cache, self.lens.numel())
+    def workspace(self, tokens, max_q):
+        return bs.kv_attention_workspace(tokens, self.heads, self.cache, self.lens.numel(), max_q)
 
     def reference(self, x, batch):
         """The attention output of the step in fp32, on the values that weights and cache stand for."""
@@ -119,12 +119,12 @@ def serve(block, prompt_lens, steps, check=False, seed=1):
     T = sum(prompt_lens)
     x = torch.randn((T, hidden), generator=gen, device="cuda").to(torch.bfloat16)
     y, batch, o = block.step(x, torch.tensor(prompt_lens, dtype=torch.int32, device="cuda"),
-                             max(prompt_lens), block.workspace(T))
+                             max(prompt_lens), block.workspace(T, max(prompt_lens)))
     if check:
         worst = max(worst, compare(x, batch, o))
     x = y[batch.q_starts[1:].long() - 1].contiguous()
 
-    one, workspace = torch.ones(R, dtype=torch.int32, device="cuda"), block.workspace(R)
+    one, workspace = torch.ones(R, dtype=torch.int32, device="cuda"), block.workspace(R, 1)
     state = block.lens.clone(), block.begin.clone()
     side = torch.cuda.Stream()  # a step outside the graph first, undone after
     side.wait_stream(torch.cuda.current_stream())

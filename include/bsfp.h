@@ -441,15 +441,16 @@ bsfp_status bsfp_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* 
  *   or NULL
  *   max_q: no request has more new tokens than this (host knowledge that
  *   sizes the launch; rows past it are not written)
- *   workspace: bsfp_kv_attention_workspace_bytes(...) bytes, 16-byte
- *   aligned, contents ignored; calls in flight at the same time need
- *   separate ones
+ *   workspace: bsfp_kv_attention_workspace_bytes(min(tokens, max_q), ...)
+ *   bytes, 16-byte aligned, contents ignored; calls in flight at the same
+ *   time need separate ones
  * Products run on the matrix cores with fp32 sums; maxima, sums and lse are
  * fp32.  Results are the same on every call (no atomics).
  * Errors: BSFP_ERR_ARG for bad pointers, shapes, strides, max_q < 1, a scale
- * that is not positive or not finite times log2 e, or a small workspace; BSFP_ERR_UNSUPPORTED for formats or head dimensions
- * outside the above, heads not a multiple of kv_heads, more than 2^31 - 1
- * rows, or a table of more than 2^31 - 8192 keys (max_pages * page_size).
+ * that is not positive or not finite times log2 e, or a small workspace;
+ * BSFP_ERR_UNSUPPORTED for formats or head dimensions outside the above,
+ * heads not a multiple of kv_heads, more than 2^31 - 1 rows, or a table of
+ * more than 2^31 - 8192 keys (max_pages * page_size).
  */
 bsfp_status bsfp_kv_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int32_t heads,
                               const bsfp_kv_cache* cache, const int32_t* block_table,
@@ -460,8 +461,9 @@ bsfp_status bsfp_kv_attention(const uint16_t* q, int64_t q_stride, int64_t token
 
 /*
  * Workspace bytes that suffice for every bsfp_kv_attention call with at most
- * these many tokens and requests, any lengths and any max_q; 0 for
- * unsupported arguments.
+ * these many tokens and requests, any lengths and any max_q; for calls whose
+ * max_q is smaller than tokens it may be given as `tokens` (a decode step,
+ * max_q = 1, needs far less).  0 for unsupported arguments.
  */
 size_t bsfp_kv_attention_workspace_bytes(int64_t tokens, int32_t heads, int32_t kv_heads,
                                          int32_t head_dim, int32_t requests);
