@@ -76,10 +76,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // ------------------------------------------------------- rows of the cache
 
-// Words of codes per lane and row (a quarter of D columns).
-template <int D>
-constexpr int kv_words() { return D / 32; }
-
+// W words of codes: a lane's quarter of a row has D / 32.
 template <int W>
 struct Words { uint32_t w[W]; };
 
@@ -416,13 +413,6 @@ __device__ __forceinline__ int64_t dpp64(int64_t v) {  // 0 from lanes outside
   const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
   const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, 0xF, 0xF, false);
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
-}
-
-// A value that all lanes of a wave hold, as a scalar.
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
-  return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
 // Lane `from`'s value, as a scalar.
