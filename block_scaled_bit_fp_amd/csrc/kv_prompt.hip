@@ -152,14 +152,13 @@ template <int D>
 struct Row {
   Words<D / 32> w;
   uint32_t s;
-  bool ok, parted;  // bits 0 and 1 of s_ok; parted is the same in all lanes
+  bool ok;
 };
 
 template <int MODE, int D>
 __device__ __forceinline__ void load_row(const KvParams& p, const KvSide& side, int head, int key,
                                          int page, int qd, Row<D>& r) {
   r.ok = page >= 0 && page < p.pages;
-  r.parted = false;
   const int64_t row = cache_row(p, r.ok ? page : 0, head, key & ((1 << p.page_shift) - 1));
   constexpr int B = scale_bytes<MODE, D>();
   r.w = load_codes<D>(side.codes + row * (D / 2), 0, qd);
@@ -356,9 +355,11 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
         have_nb = true;
       }
     };
+    bool parted = false;  // bit 1 of s_ok for the wave's rows of the tile being staged
     // Before tile t is staged; tiles that all rows see whole go without.
     auto part_values = [&](Row<D>& r, int t) {
       if constexpr (kFlags > 0) {
+        parted = false;
         if (t >= full0 && t < full1) return;
         const int key = t * kTile + skey;
         const uint32_t bad =
@@ -369,7 +370,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
           const uint64_t lanes = __ballot(bad >> (8 * j + 7) & 1u);
           if (lane == 0) s_bad[t & 1][j][wave] = lanes;
         }
-        r.parted = true;
+        parted = true;
         r.s = without<MODE>(r.s, bad);
       }
     };
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
         *reinterpret_cast<u32x4_t*>(vr + v_piece<D>(sq, j) * 8) =
             decode_value_word<MODE, D>(seen ? r.w.w[j] : 0u, vs, j, nb);
       if (j0 == 0 && lane == 0)
-        reinterpret_cast<uint8_t*>(&s_ok[at])[wave] = r.ok | (kFlags > 0 && r.parted) << 1;
+        reinterpret_cast<uint8_t*>(&s_ok[at])[wave] = r.ok | (kFlags > 0 && parted) << 1;
     };
     // The columns 16 j .. of the keys 32 u .. of tile t, as an operand.
     auto key_operand = [&](int at, int i) {
