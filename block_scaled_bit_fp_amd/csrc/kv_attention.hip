@@ -93,6 +93,19 @@ __device__ __forceinline__ Work request_work(const KvParams& p, const KvRequest&
   return w;
 }
 
+// o += v (hi + lo)^T, bf16.  In place by hand: the builtin on a path of its own
+// made the compiler copy the sums (28 registers spilled at MXFP4, D = 128).
+// With the waits that it would put around: 16 cycles until the sums are there.
+__device__ __forceinline__ void add_wide(f32x4_t& o, u32x4_t v, u32x4_t hi, u32x4_t lo) {
+  asm volatile(
+      "s_nop 7\n\t"
+      "v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0\n\t"
+      "s_nop 15\n\t"
+      "v_mfma_f32_16x16x32_bf16 %0, %1, %3, %0\n\t"
+      "s_nop 15"
+      : "+v"(o) : "v"(v), "v"(hi), "v"(lo));
+}
+
 // A tile's keys or values as loaded: two runs of 16 rows.
 template <int MODE, int D>
 struct Keys {
@@ -393,7 +406,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
         }
         if constexpr (kFlags > 0) {
           const uint32_t bad[2] = {not_finite<MODE>(v.s[0]), not_finite<MODE>(v.s[1])};
-          if (q.q_len > 1 && __any(bad[0] | bad[1])) {
+          if (__builtin_expect(q.q_len > 1 && __any(bad[0] | bad[1]), 0)) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const uint32_t seen = keys_seen(key0 + u * 16, lo, hi);
@@ -409,11 +422,25 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
           }
         }
       }
+      bool wide = false;  // some values are left out and added at the end of the tile
       if constexpr (MODE != BSFP_NVFP4) {  // room for the tile's values in fp16
-        const int x = max(value_exponent<MODE, D>(v.s[0]), value_exponent<MODE, D>(v.s[1]));
-        if (!have_nb || __any(x + nb > kValueExpMax)) {
+        const int x0 = value_exponent<MODE, D>(v.s[0]), x1 = value_exponent<MODE, D>(v.s[1]);
+        const int x = max(x0, x1);
+        if (__builtin_expect(!have_nb || __any(x + nb > kValueExpMax), 0)) {
           const int mx = row_max(x);
-          const int to = !have_nb ? value_shift(mx) : mx + nb > kValueExpMax ? value_shift(mx) : nb;
+          int to = !have_nb ? value_shift(mx) : mx + nb > kValueExpMax ? value_shift(mx) : nb;
+          if (edge && q.q_len > 1) {
+            // the scale in use, or that of the tile's smallest values but zero
+            const int least = row_min(min(x0 ? x0 : 255, x1 ? x1 : 255));
+            const int at = have_nb ? nb : value_shift(min(least, mx));
+            wide = __any(mx + at > kValueExp + kValueSpread);
+            if (wide) {
+              to = at;
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                if ((u ? x1 : x0) + at > kValueExpMax) v.s[u] = 0;
+            }
+          }
           if (have_nb) {
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -451,7 +478,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
         m = mx;
       }
       float shift = m == -INFINITY ? 0.0f : kOffset - m * c;
-      if (__any(fabsf(shift) > kFar)) {
+      if (__builtin_expect(__any(fabsf(shift) > kFar), 0)) {
         const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] -= base;
@@ -484,6 +511,47 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
         step_end();
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if constexpr (MODE != BSFP_NVFP4) {
+        if (__builtin_expect(wide, 0)) {  // the values that were left out
+          uint32_t scales[2];
+          int mx = 0;
+          bool large[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int64_t row = max(rows_now.row[u], (int64_t)0) * scale_bytes<MODE, D>();
+            scales[u] = load_scales<MODE, D>(p.v.scales + row, p.v.biases + row, n, qd);
+            const int key = key0 + u * 16 + n, x = value_exponent<MODE, D>(scales[u]);
+            large[u] = rows_now.row[u] >= 0 && key >= any_lo && key < any_hi &&
+                       x + nb > kValueExpMax && !not_finite<MODE>(scales[u]);
+            if (large[u]) mx = max(mx, x);
+          }
+          const int to = value_shift_wide(nb, row_max(mx));
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+            o[d] *= ldexpf(1.0f, __builtin_amdgcn_readlane(to - nb, (d * 64 / D) * 16));
+          nb = to;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const Words<W> w =
+                load_codes<D>(p.v.codes + max(rows_now.row[u], (int64_t)0) * (D / 2), n, qd);
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              *reinterpret_cast<u32x4_t*>(vt + (u * 16 + n) * v_stride<D>() + qd * (D / 4) + j * 8) =
+                  large[u] ? decode_value_wide<MODE, D>(w.w[j], scales[u], j, nb)
+                           : u32x4_t{0, 0, 0, 0};
+              step_end();
+            }
+          }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          const u32x4_t hi = wide_probabilities<false>(pf), lo = wide_probabilities<true>(pf);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            add_wide(o[d], value_operand(d), hi, lo);
+            step_end();
+          }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+      }
     };
     for (; tile < tile_end; tile += 2 * step) {
       use_tile(tile, k0, v0, rows0);

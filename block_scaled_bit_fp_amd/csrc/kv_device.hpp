@@ -265,6 +265,52 @@ constexpr int kValueExp = 127 + 8, kValueExpMax = 127 + 13;
 // The nb for a quarter whose largest biased exponent is e.
 __device__ __forceinline__ int value_shift(int e) { return min(kValueExp - e, 120); }
 
+// A key that only some rows see must not cost the others their bits, and would
+// where its values are so much larger that a common nb takes the rest of the
+// tile out of fp16.  Where the exponents of a tile that some rows do not see
+// whole pass the present scale by kValueSpread, the quarters of rows that do not
+// fit it are left out at first and then added by themselves: as bf16, which has
+// the range (exact for MXFP4; affine ones keep 8 bits), with the probabilities
+// as the sum of two bf16.  nb then falls only as far as it must for fp32:
+// products of probabilities with values up to 2^115; still larger values are
+// finite themselves, so that a probability of zero takes them out.
+constexpr int kValueSpread = 12, kValueExpWide = 230, kValueExpTop = 242;
+__device__ __forceinline__ int value_shift_wide(int nb, int e) {
+  return min(nb, kValueExpWide - min(e, kValueExpTop));
+}
+// Probabilities (fp16) as bf16, or what that leaves of their 11 bits.
+template <bool REST>
+__device__ __forceinline__ u32x4_t wide_probabilities(u32x4_t p) {
+  u32x4_t o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = p[i];  // (a cast of an element in place takes element 0)
+    const f16x2_t f = __builtin_bit_cast(f16x2_t, w);
+    const float a = (float)f.x, b = (float)f.y;
+    o[i] = pack_bf16x2(a, b);
+    if constexpr (REST) o[i] = pack_bf16x2(a - bf16_lo(o[i]), b - bf16_hi(o[i]));
+  }
+  return o;
+}
+// Values: word j as four bf16 pairs, times 2^nb.
+template <int MODE, int D>
+__device__ __forceinline__ u32x4_t decode_value_wide(uint32_t w, uint32_t scales, int j, int nb) {
+  u32x4_t o;
+  if constexpr (MODE == BSFP_MXFP4) {
+    const float s = ldexpf(1.0f, e8m0_byte<D>(scales, j) - 127 + nb);
+    o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+    o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+    o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+    o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+  } else {
+    const float s = ldexpf(bf16_lo(scales), nb), b = ldexpf(bf16_hi(scales), nb);
+    auto value = [&](int i) { return __builtin_fmaf((float)(w >> (4 * i) & 15u), s, b); };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(value(2 * i), value(2 * i + 1));
+  }
+  return o;
+}
+
 // A word of affine codes as bf16 integers, columns in the order
 // 0 2 4 6 1 3 5 7 (the nibbles of even and odd columns are split by one mask).
 __device__ __forceinline__ u32x4_t decode_codes_split(uint32_t w) {
@@ -289,12 +335,13 @@ __device__ __forceinline__ float quad_max(float v) {
       u32x2_t, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
   return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
 }
-// Maximum over each group of 16 lanes.
+// Maximum and minimum over each group of 16 lanes.
 __device__ __forceinline__ int row_max(int v) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) v = max(v, __shfl_xor(v, o, 64));
   return v;
 }
+__device__ __forceinline__ int row_min(int v) { return -row_max(-v); }
 __device__ __forceinline__ float quad_sum(float v) {
   u32x2_t r = __builtin_bit_cast(
       u32x2_t, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));

@@ -70,6 +70,19 @@ __device__ __forceinline__ f32x16_t mma32_f16(u32x4_t a, u32x4_t b, f32x16_t c) 
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
                                                 __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
+// o += v (hi + lo)^T, bf16; by hand as in kv_attention.hip (58 registers spilled
+// at MXFP4, D = 128), with 32 cycles until the sums are there.
+__device__ __forceinline__ void add_wide(f32x16_t& o, u32x4_t v, u32x4_t hi, u32x4_t lo) {
+  asm volatile(
+      "s_nop 7\n\t"
+      "v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\t"
+      "s_nop 15\n\t"
+      "s_nop 15\n\t"
+      "v_mfma_f32_32x32x16_bf16 %0, %1, %3, %0\n\t"
+      "s_nop 15\n\t"
+      "s_nop 15"
+      : "+v"(o) : "v"(v), "v"(hi), "v"(lo));
+}
 template <int MODE>
 __device__ __forceinline__ f32x16_t mma32_keys(u32x4_t a, u32x4_t b, f32x16_t c) {
   if constexpr (MODE == BSFP_NVFP4) return mma32_f16(a, b, c);
@@ -174,7 +187,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
   __shared__ __align__(16) Buffers<D> buf;
   __shared__ float s_scale[kAffine ? 2 : 1][kAffine ? G64 : 1][kTile];
   __shared__ float s_bias[kAffine ? 2 : 1][kAffine ? G64 : 1][kTile];
-  __shared__ int s_exp[2][4][kWaves];
+  __shared__ int s_exp[2][4][kWaves], s_least[4][kWaves];
   // a byte for each 16 keys (a wave stages them).  Bit 0: their page is one of
   // the cache's.  Bit 1: some of their values are not finite and taken as zero;
   // s_bad: lane 4 (key % 16) + quarter of the columns, by group of the quarter
@@ -328,31 +341,68 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
     // V of quarter x of the columns is held times 2^nb: in O, in the tile in use
     // and in the tile being staged
     int nb_o[4] = {0, 0, 0, 0}, nb_now[4] = {0, 0, 0, 0}, nb_next[4] = {0, 0, 0, 0};
-    bool have_nb = false;
+    bool wide_now = false, wide_next = false;  // some values are left out and added at the end
 
     const int t_end = tile0 + b;
     auto page_of = [&](int t) {
       const int key = t * kTile + skey;
       return t < t_end && key < q.last ? table[key >> p.page_shift] : -1;
     };
-    auto publish = [&](const Row<D>& r, int t) {  // the tile's largest exponents
+    // Of the quarter that the thread stages.  By value: of an array the compiler
+    // would make the choice by address, and keep the array in memory.
+    auto own = [&](int x0, int x1, int x2, int x3) {
+      return sq < 2 ? (sq ? x1 : x0) : (sq == 2 ? x2 : x3);
+    };
+    auto largest = [](const int (&x)[kWaves]) {
+      return __builtin_amdgcn_readfirstlane(max(max(x[0], x[1]), max(x[2], x[3])));
+    };
+    // The tile's largest exponents; of the first tile also the least but zero.
+    auto publish = [&](const Row<D>& r, int t, bool first) {
       if constexpr (MODE != BSFP_NVFP4) {
         const int key = t * kTile + skey;
         int e = r.ok && key >= all.any_lo && key < all.any_hi ? value_exponent<MODE, D>(r.s) : 0;
+        int least = e ? e : 255;
 #pragma unroll
         for (int x = 4; x < 64; x <<= 1) e = max(e, __shfl_xor(e, x, 64));
         if (lane < 4) s_exp[t & 1][lane][wave] = e;
+        if (first) {
+#pragma unroll
+          for (int x = 4; x < 64; x <<= 1) least = min(least, __shfl_xor(least, x, 64));
+          if (lane < 4) s_least[lane][wave] = least;
+        }
       }
     };
-    auto settle = [&](int t) {  // after the barrier that follows publish
+    // After the barrier that follows publish: the tile's powers of two.
+    auto settle = [&](Row<D>& r, int t, bool first) {
       if constexpr (MODE != BSFP_NVFP4) {
+        int e[4], top = 0;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int* e4 = s_exp[t & 1][x];
-          const int e = __builtin_amdgcn_readfirstlane(max(max(e4[0], e4[1]), max(e4[2], e4[3])));
-          if (!have_nb || e + nb_next[x] > kValueExpMax) nb_next[x] = value_shift(e);
+          e[x] = largest(s_exp[t & 1][x]);
+          top = max(top, e[x] + nb_next[x]);
         }
-        have_nb = true;
+        wide_next = false;
+        if (__builtin_expect(!first && !wide_now && top <= kValueExpMax, 1)) return;
+        int at[4];
+        top = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          at[x] = nb_next[x];
+          if (first) {
+            const int* l4 = s_least[x];
+            at[x] = value_shift(min(
+                __builtin_amdgcn_readfirstlane(min(min(l4[0], l4[1]), min(l4[2], l4[3]))), e[x]));
+          } else if (wide_now) {  // what becomes of it at the end of the tile in use
+            at[x] = value_shift_wide(at[x], largest(s_exp[(t + 1) & 1][x]));
+          }
+          top = max(top, e[x] + at[x]);
+        }
+        wide_next = top > kValueExp + kValueSpread && !(t >= full0 && t < full1);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          nb_next[x] = !wide_next && (first || e[x] + at[x] > kValueExpMax) ? value_shift(e[x]) : at[x];
+        const int nb = own(nb_next[0], nb_next[1], nb_next[2], nb_next[3]);
+        if (wide_next && value_exponent<MODE, D>(r.s) + nb > kValueExpMax) r.s = 0;
       }
     };
     bool parted = false;  // bit 1 of s_ok for the wave's rows of the tile being staged
@@ -360,11 +410,11 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
     auto part_values = [&](Row<D>& r, int t) {
       if constexpr (kFlags > 0) {
         parted = false;
-        if (t >= full0 && t < full1) return;
+        if (__builtin_expect(t >= full0 && t < full1, 1)) return;
         const int key = t * kTile + skey;
         const uint32_t bad =
             r.ok && key >= all.any_lo && key < all.any_hi ? not_finite<MODE>(r.s) : 0u;
-        if (!__any(bad)) return;
+        if (__builtin_expect(!__any(bad), 1)) return;
 #pragma unroll
         for (int j = 0; j < kFlags; ++j) {
           const uint64_t lanes = __ballot(bad >> (8 * j + 7) & 1u);
@@ -373,6 +423,25 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
         parted = true;
         r.s = without<MODE>(r.s, bad);
       }
+    };
+    auto rescale = [&](const int (&to)[4]) {  // of O, to other powers of two
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (nb_o[x] != to[x]) {
+          const float f = ldexpf(1.0f, to[x] - nb_o[x]);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            if constexpr (D == 64) {  // a quarter is half of a 32-column tile
+              if (d == x / 2) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[d][(x & 1) * 8 + i] *= f;
+              }
+            } else {
+              if (d / (D / 128) == x) o[d] *= f;
+            }
+          }
+          nb_o[x] = to[x];
+        }
     };
     auto stage_k = [&](const Row<D>& r, int t, int j0, int j1) {  // words [j0, j1)
       const int at = t & 1;
@@ -397,9 +466,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
       // a key that no row sees: a value of zero, whatever the page holds
       const bool seen = r.ok && key >= all.any_lo && key < all.any_hi;
       const uint32_t vs = seen ? r.s : 0u;
-      const int nb = MODE == BSFP_NVFP4 ? 0
-                     : sq < 2           ? (sq ? nb_next[1] : nb_next[0])
-                                        : (sq == 2 ? nb_next[2] : nb_next[3]);
+      const int nb = MODE == BSFP_NVFP4 ? 0 : own(nb_next[0], nb_next[1], nb_next[2], nb_next[3]);
       uint16_t* vr = buf.v[at] + skey * v_stride<D>() + sq * (D / 4);
 #pragma unroll
       for (int j = j0; j < j1; ++j)
@@ -449,29 +516,53 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
     load_row<MODE, D>(p, p.k, head, t * kTile + skey, page, sq, rk);
     load_row<MODE, D>(p, p.v, head, t * kTile + skey, page, sq, rv);
     page = page_of(t + 1);
-    publish(rv, t);
+    publish(rv, t, true);
     if constexpr (MODE != BSFP_NVFP4) __syncthreads();
-    settle(t);
+    settle(rv, t, true);
     part_values(rv, t);
     stage_k(rk, t, 0, W);
     stage_v(rv, t, 0, W);
     load_row<MODE, D>(p, p.k, head, (t + 1) * kTile + skey, page, sq, rk);
     load_row<MODE, D>(p, p.v, head, (t + 1) * kTile + skey, page, sq, rv);
     page = page_of(t + 2);
-    publish(rv, t + 1);
+    publish(rv, t + 1, false);
     for (; t < t_end; ++t) {
       __syncthreads();
       const int at = t & 1, key0 = t * kTile;
 #pragma unroll
       for (int x = 0; x < 4; ++x) nb_now[x] = nb_next[x];
-      settle(t + 1);
+      wide_now = wide_next;
+      settle(rv, t + 1, false);
       part_values(rv, t + 1);
       auto load = [&]() {
         load_row<MODE, D>(p, p.k, head, (t + 2) * kTile + skey, page, sq, rk);
         load_row<MODE, D>(p, p.v, head, (t + 2) * kTile + skey, page, sq, rv);
         page = page_of(t + 3);
       };
-      if (key0 < mine.any_hi && key0 + kTile > mine.any_lo) {  // some row of the wave sees some key
+      // O^T: in steps of 16 keys, 4 half .. + 3 and 8 + 4 half .. + 3 of each in
+      // both operands
+      const uint16_t* vr = buf.v[at] + (half * 4 + ((lane & 15) >> 2)) * v_stride<D>();
+      const int piece = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);  // of 32 columns
+      auto value_operand = [&](int i) {
+        const uint16_t* r = vr + i / DT * 16 * v_stride<D>() + i % DT * 32 +
+                            v_piece<D>(i % DT, piece) * 8 + (lane & 1) * 4;
+        const u32x2_t v0 = lds_read_transposed(r);
+        const u32x2_t v1 = lds_read_transposed(r + 8 * v_stride<D>());
+        return u32x4_t{v0.x, v0.y, v1.x, v1.y};
+      };
+      // What the exponents are fma(S, c, .) of; past kFar S gets the maximum taken off.
+      auto shifted = [&](f32x16_t (&sc)[2]) {
+        const float shift = m == -INFINITY ? 0.0f : kOffset - m * c;
+        if (__builtin_expect(__any(fabsf(shift) > kFar), 0)) {
+          const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sc[i >> 4][i & 15] -= base;
+          return kOffset;
+        }
+        return shift;
+      };
+      const bool any_seen = key0 < mine.any_hi && key0 + kTile > mine.any_lo;  // by the wave's rows
+      if (any_seen) {
         f32x16_t sc[2];
         u32x4_t kf[2 * KS];
 #pragma unroll
@@ -500,7 +591,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
         const uint32_t ok = __builtin_amdgcn_readfirstlane(s_ok[at]);
         if (key0 < mine.all_lo || key0 + kTile > mine.all_hi || ok != 0x01010101u) {
           if constexpr (kFlags > 0) {
-            if (ok & 0x02020202u) {
+            if (__builtin_expect(ok & 0x02020202u, 0)) {
 #pragma unroll
               for (int j = 0; j < kFlags; ++j) {
                 uint64_t quarters = 0;  // four bits a key
@@ -540,43 +631,8 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
           for (int d = 0; d < DT; ++d) o[d] *= f;
           m = mx;
         }
-        if constexpr (MODE != BSFP_NVFP4) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (nb_o[x] != nb_now[x]) {
-              const float f = ldexpf(1.0f, nb_now[x] - nb_o[x]);
-#pragma unroll
-              for (int d = 0; d < DT; ++d) {
-                if constexpr (D == 64) {  // a quarter is half of a 32-column tile
-                  if (d == x / 2) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[d][(x & 1) * 8 + i] *= f;
-                  }
-                } else {
-                  if (d / (D / 128) == x) o[d] *= f;
-                }
-              }
-              nb_o[x] = nb_now[x];
-            }
-        }
-        float shift = m == -INFINITY ? 0.0f : kOffset - m * c;
-        if (__any(fabsf(shift) > kFar)) {
-          const float base = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sc[i >> 4][i & 15] -= base;
-          shift = kOffset;
-        }
-        // O^T: in steps of 16 keys, 4 half .. + 3 and 8 + 4 half .. + 3 of each
-        // in both operands
-        const uint16_t* vr = buf.v[at] + (half * 4 + ((lane & 15) >> 2)) * v_stride<D>();
-        const int piece = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);  // of 32 columns
-        auto value_operand = [&](int i) {
-          const uint16_t* r = vr + i / DT * 16 * v_stride<D>() + i % DT * 32 +
-                              v_piece<D>(i % DT, piece) * 8 + (lane & 1) * 4;
-          const u32x2_t v0 = lds_read_transposed(r);
-          const u32x2_t v1 = lds_read_transposed(r + 8 * v_stride<D>());
-          return u32x4_t{v0.x, v0.y, v1.x, v1.y};
-        };
+        if constexpr (MODE != BSFP_NVFP4) rescale(nb_now);
+        const float shift = shifted(sc);
         u32x4_t pf[4], vf[4 * DT];
         auto probabilities = [&](int k) {  // pair k of 16
           const int x = k / 4, e = (x & 1) * 8 + 2 * (k % 4);
@@ -606,7 +662,65 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
         stage_v(rv, t + 1, 0, W);
         load();
       }
-      publish(rv, t + 2);
+      if constexpr (MODE != BSFP_NVFP4) {
+        if (__builtin_expect(wide_now, 0)) {  // the values that were left out
+          int to[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) to[x] = value_shift_wide(nb_now[x], largest(s_exp[at][x]));
+          __syncthreads();  // all waves are done with the tile
+          const int key = key0 + skey;
+          Row<D> r;
+          load_row<MODE, D>(p, p.v, head, key, page_of(t), sq, r);
+          const int nb = own(nb_now[0], nb_now[1], nb_now[2], nb_now[3]);
+          const int nb_wide = own(to[0], to[1], to[2], to[3]);
+          const bool large = r.ok && key >= all.any_lo && key < all.any_hi &&
+                             !not_finite<MODE>(r.s) && value_exponent<MODE, D>(r.s) + nb > kValueExpMax;
+          uint16_t* row = buf.v[at] + skey * v_stride<D>() + sq * (D / 4);
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+            *reinterpret_cast<u32x4_t*>(row + v_piece<D>(sq, j) * 8) =
+                large ? decode_value_wide<MODE, D>(r.w.w[j], r.s, j, nb_wide) : u32x4_t{0, 0, 0, 0};
+          __syncthreads();
+          if (any_seen) {
+            rescale(to);
+            // the probabilities once more: keeping them would take registers in
+            // every tile
+            f32x16_t sc[2];
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i) {
+              score(at, i, key_operand(at, i), sc);
+              step_end();
+            }
+            const uint32_t ok = __builtin_amdgcn_readfirstlane(s_ok[at]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int at16 = u * 32 + (i >> 2) * 8 + half * 4 + (i & 3), k = key0 + at16;
+                if (!(ok >> ((u * 2 + (i >> 3)) * 8) & 1) || k < lo || k >= hi)
+                  sc[u][i] = -INFINITY;
+              }
+            const float shift = shifted(sc);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {  // 16 keys
+              u32x4_t pf;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int e = (x & 1) * 8 + 2 * k;
+                pf[k] = pack_f16x2(__builtin_amdgcn_exp2f(__builtin_fmaf(sc[x >> 1][e], c, shift)),
+                                   __builtin_amdgcn_exp2f(__builtin_fmaf(sc[x >> 1][e + 1], c, shift)));
+              }
+              const u32x4_t hi = wide_probabilities<false>(pf), lo = wide_probabilities<true>(pf);
+#pragma unroll
+              for (int d = 0; d < DT; ++d) {
+                add_wide(o[d], value_operand(x * DT + d), hi, lo);
+                step_end();
+              }
+            }
+          }
+        }
+      }
+      publish(rv, t + 2, false);
     }
 
     // ---- out, or the partial state

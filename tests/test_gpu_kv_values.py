@@ -134,3 +134,48 @@ def test_window_and_max_q_beyond_32_bits(bsfp):
         with pytest.raises(bsfp.BsfpError) as ei:
             bsfp.kv_attention(q, cache, batch, **bad)
         assert ei.value.status == 1
+
+
+def put(bsfp, cache, batch, r, t, P, v):
+    """The key t of request r: some K (the same each time) and the values v."""
+    slot = batch.block_table[r, t // P].long().view(1) * P + t % P
+    bsfp.kv_append(cache, rand(v.shape, t + 1), v, slot)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 30, 2.0 ** 60, 1e30, 3e38, float("inf")])
+@pytest.mark.parametrize("kv,q_lens,heads,window", [
+    ([100, 61], [4, 7], 4, 0), ([100, 40], [16, 3], 1, 5), ([12, 9], [12, 9], 1, 0), ([260, 200], [70, 40], 4, 0),
+    ([300, 129], [129, 60], 1, 0), ([300, 129], [129, 60], 2, 20), ([400, 250], [200, 90], 1, 70), ([1500], [12], 4, 0),
+    ([2100], [4], 4, 0)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_huge_values_reach_only_the_rows_that_see_them(bsfp, mode, size, kv, q_lens, heads, window, D):
+    """Two new tokens, one of them a million times larger, with values far beyond the others': rows that do not
+    see them are, within the tolerance, those over the values that they do see; the huge ones themselves come
+    through to the rows that see them, to 7 bits."""
+    P, scale = 32, float(np.float32(1.0 / np.sqrt(D)))
+    cols = [7, D - 28]
+    cache, batch, q = build(bsfp, mode, kv, q_lens, heads, 1, D, P, seed=heads + q_lens[0])
+    starts = np.concatenate([[0], np.cumsum(q_lens)])
+    sees = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
+    huge = [(r, kv[r] - n + at, s) for r, n in enumerate(q_lens) for at, s in ((n // 3, size / 2 ** 20), (n // 2, size))]
+    for r, t, s in huge:
+        v = rand((1, 1, D), t)
+        v[0, 0, cols] = s
+        put(bsfp, cache, batch, r, t, P, v)
+        pos = torch.arange(q_lens[r], device="cuda") + kv[r] - q_lens[r]
+        sees[starts[r]:starts[r + 1]] |= (pos >= t) & (pos < t + window if window else pos >= t)
+    out, lse = bsfp.kv_attention(q, cache, batch, window=window, return_lse=True)
+    got, sees = out.double().cpu().numpy(), sees.cpu().numpy()
+    assert not torch.isnan(lse).any() and not sees.all() and sees.any()
+    if size <= 1e30:
+        want, _, tol, _ = ref.attention(q, cache, batch.block_table, batch.kv_lens, batch.q_starts, scale, window)
+        # the tolerance holds 2^-11 of the sum of probabilities times |V| at least
+        assert (np.abs(got - want)[sees][..., cols] <= 16 * tol[sees][..., cols]).all()
+    # the reference over a cache in which those keys' values are small ones, and the same keys
+    for r, t, _ in huge:
+        put(bsfp, cache, batch, r, t, P, rand((1, 1, D), t))
+    want, wlse, tol, ltol = ref.attention(q, cache, batch.block_table, batch.kv_lens, batch.q_starts, scale, window)
+    err = np.abs(got - want)[~sees]
+    assert (err <= tol[~sees]).all(), err.max()
+    assert (np.abs(lse.double().cpu().numpy() - wlse) <= ltol).all()
