@@ -219,9 +219,13 @@ constexpr int wgs_per_cu(int mode, int D) {
                     : (mode == BSFP_AFFINE ? 1 : 2);
 }
 
-template <int MODE, int D>
+// ONE: no request has more than one new token (a decode step), so that all rows
+// of a segment see the same keys and nothing need be told apart by row.  Us with
+// it and with the general one: 64 requests of 512..8192 keys, NVFP4 44.0 and 44.4,
+// MXFP4 39.6 and 39.8, affine 58.3 and 59.4; 40 of 551..4029, MXFP4, 22.6 and 24.0.
+template <int MODE, int D, bool ONE>
 __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel(KvParams p, KvParts parts) {
-  constexpr int W = D / 32, DT = D / 16, G64 = D / 64, kFlags = kGroupFlags<MODE, D>;
+  constexpr int W = D / 32, DT = D / 16, G64 = D / 64, kFlags = ONE ? 0 : kGroupFlags<MODE, D>;
   __shared__ __align__(16) uint8_t lds[split_lds_bytes<D>()];
   __shared__ float s_ml[kWaves][2][kRows];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, qd = lane >> 4;
@@ -429,7 +433,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
         if (__builtin_expect(!have_nb || __any(x + nb > kValueExpMax), 0)) {
           const int mx = row_max(x);
           int to = !have_nb ? value_shift(mx) : mx + nb > kValueExpMax ? value_shift(mx) : nb;
-          if (edge && q.q_len > 1) {
+          if (!ONE && edge && q.q_len > 1) {
             // the scale in use, or that of the tile's smallest values but zero
             const int least = row_min(min(x0 ? x0 : 255, x1 ? x1 : 255));
             const int at = have_nb ? nb : value_shift(min(least, mx));
@@ -511,7 +515,7 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
         step_end();
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if constexpr (MODE != BSFP_NVFP4) {
+      if constexpr (MODE != BSFP_NVFP4 && !ONE) {
         if (__builtin_expect(wide, 0)) {  // the values that were left out
           uint32_t scales[2];
           int mx = 0;
@@ -750,7 +754,11 @@ template <int MODE, int D>
 hipError_t run(const KvParams& p, void* ws, hipStream_t s) {
   JoinSide split = {{}, std::min(device_cu_count() * wgs_per_cu(MODE, D), kMaxRuns), kRows};
   split.parts = kv_parts(ws, split.runs, kRows, D);
-  hipLaunchKernelGGL((kv_split_kernel<MODE, D>), dim3(split.runs), dim3(kThreads), 0, s, p, split.parts);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(split.runs), dim3(kThreads), 0, s, p, split.parts);
+  };
+  if (std::min(p.max_q, p.tokens) == 1) go(kv_split_kernel<MODE, D, true>);
+  else go(kv_split_kernel<MODE, D, false>);
   hipError_t e = hipGetLastError();
   int live = (int)std::min<int64_t>((int64_t)p.max_q * p.group, kRows);
   // the longest segment there can be; none is cut up to kWhole tiles
