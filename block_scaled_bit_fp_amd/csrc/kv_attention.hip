@@ -28,10 +28,12 @@
 // second kernel joins them in the order of the line.
 //
 // Measured (kernel alone, NVFP4, 64 query heads over 8 kv heads of 128): 64
-// requests of 512..8192 keys, 211 MB: 43.4 us, 4.9 TB/s; one of 131077 keys,
-// 151 MB: 32.3 us, 4.7 TB/s; one of 259 keys: 8.9 us, a chain of loads and cold
-// instructions.  256 requests, window 128, MXFP4, 64-wide heads: 15.9 us.
-// Affine, 32 heads over 32, 134 MB: 43.4 us, bound by the decoding.
+// requests of 512..8192 keys, 211 MB: 43.3 us, 4.9 TB/s; one of 131077 keys,
+// 151 MB: 31.3 us, 4.8 TB/s; one of 259 keys: 8.9 us, a chain of loads and cold
+// instructions.  256 requests, window 128, MXFP4, 64-wide heads: 15.8 us; most
+// runs hold two short segments, one wave each, and the other two waves idle.
+// Affine, 32 heads over 32, 134 MB: 41.9 us; vector issue is 59 % busy, mostly
+// with decoding, and two waves per SIMD do not cover the rest.
 #include <algorithm>
 
 #include "kv_device.hpp"
@@ -44,21 +46,23 @@ constexpr int kTile = 32;       // keys per step of a wave
 constexpr int kRows = kSplitRows;  // query rows of a segment
 
 // All in tiles.  Each was measured on both sides (us, split kernel + join; A: 64
-// requests of 512..8192 keys; B: 43 of 139..1116 keys, 64-wide heads; C: one of
-// 29088 keys, MXFP4; E: 256 with a window of 128, MXFP4, 64-wide heads).
-// The shortest run.  4: C 7.2 + 5.7; 8: C 7.8 + 4.7, and 20 requests of up to
-// 800 affine keys, whose segments then queue in one run, 15.6 instead of 12.8.
+// requests of 512..8192 keys; B: 43 of 143..1097 keys, one 64-wide head; C: one of
+// 6826 keys, MXFP4, 16 heads over 4; D: 146 of 21..169 affine keys, 16 heads over
+// 2; E: 256 with a window of 128, MXFP4, 64-wide heads).
+// The shortest run.  4: C 7.3..8.6 + 5.4, D 12.7; 8: C 8.4 + 4.3, D, whose
+// segments then queue in one run, 15.7.
 constexpr int kMinRun = 4;
-// The longest segment that is never cut.  16: A 45.9, B 10.5 + 3.9, E 15.8;
-// 8: 45.9, 11.3 + 3.9, 16.1; 32: 45.8, 12.2, 16.0.
+// The longest segment that is never cut.  16: A 43.5, B 9.4..10.2 + 4.0; 8: A
+// 43.4, B 8.0 + 4.1; 32: A 44.6, B 12.1 + 3.8; E 16.0 with all three.
 constexpr int kWhole = 16;
 // The longest segment that one wave takes, where runs are longer than the
-// shortest; else each run has about one segment, and the waves share it (B 9.1
-// instead of 11.1).  6: E 15.8; 3: E 20.4.
+// shortest; else each run has about one segment, and the waves share it (D 12.7;
+// alone there too, 15.5).  6: E 16.0; 3: E 20.1.
 constexpr int kAlone = 6;
 static_assert(kAlone <= kWhole, "one wave takes whole segments only");
 // What a segment costs beside its tiles, in tiles: it takes that much more of
-// the line.  More where the four waves share it.
+// the line.  More where the four waves share it.  None: A 51.5, C 10.6 + 5.5, D
+// 22.6, E 16.7.
 constexpr int kSegmentAlone = 4, kSegmentShared = 12;
 constexpr __device__ int segment_length(int tiles) {
   return tiles + (tiles <= kAlone ? kSegmentAlone : kSegmentShared);
@@ -95,7 +99,7 @@ __device__ __forceinline__ Work request_work(const KvParams& p, const KvRequest&
 
 // o += v (hi + lo)^T, bf16.  In place by hand: the builtin on a path of its own
 // made the compiler copy the sums (28 registers spilled at MXFP4, D = 128).
-// With the waits that it would put around: 16 cycles until the sums are there.
+// With waits longer than the products take: 16 steps until the sums are there.
 __device__ __forceinline__ void add_wide(f32x4_t& o, u32x4_t v, u32x4_t hi, u32x4_t lo) {
   asm volatile(
       "s_nop 7\n\t"

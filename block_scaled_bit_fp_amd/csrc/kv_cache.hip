@@ -228,9 +228,9 @@ constexpr int kAppendThreads = 256;
 // blockIdx.y picks K or V.  The row is asked for together with its slot, so it
 // is read whether the slot is good or not.  Row numbers are 32-bit where they
 // fit (a 64-bit division is some 150 instructions).
-//   8192 rows of 8 x 128 at scattered slots (43 MB): 12.3 us, 3.5 TB/s; bound
-// by the scale writes, 8 bytes of a row at a time.  Two words per lane: 13.5,
-// four: 14.0.
+//   8192 rows of 8 x 128 at scattered slots (43 MB): 12.4..13.3 us by card, 3.2 to
+// 3.5 TB/s; bound by the scale writes, single bytes of 8 bytes a row.  Two words
+// per lane took 1.2 us more, four 1.7.
 template <int MODE, int D>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(
     AppendSide k, AppendSide v, const int64_t* __restrict__ slots, int64_t rows, int kv_heads,
@@ -287,8 +287,9 @@ hipError_t launch_kv_plan(const int32_t* past, const int32_t* q, int requests, i
                           int64_t free_count, const int32_t* free_begin, int64_t tokens,
                           int32_t* kv_lens, int32_t* q_starts, int64_t* slots, int32_t* positions,
                           int32_t* state, int32_t* next_lens, hipStream_t s) {
-  // one request per thread: with 256 threads 1021 requests took four rounds of
-  // the scan, 10.5 us; up to 256 requests the smaller workgroup starts sooner
+  // one request per thread: with 256 threads 1021 requests take four rounds of
+  // the scan, 10.4 us instead of 7.3; up to 256 requests the smaller workgroup
+  // starts sooner
   const bool wide = requests > 256;
   const int64_t per = wide ? 2048 : 1024;
   const int64_t wgs = std::max<int64_t>(1, std::min<int64_t>((tokens + per - 1) / per,

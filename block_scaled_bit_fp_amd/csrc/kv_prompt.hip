@@ -21,10 +21,13 @@
 // are neighbours, so an XCD's L2 holds the cache of the one or two kv heads
 // that it works on.
 //
-// Measured (NVFP4, 64 query heads over 8 kv heads of 128): two chunks of
-// 1500..2048 rows over 4096..8192 keys, 626 GFLOP: 675..690 us, some 920
-// TFLOP/s (a large bf16 library product: 1230).  Matrix units 44 % busy, vector
-// issue 64 %, no LDS bank conflicts; bound by the vector work beside the products.
+// Measured (64 query heads over 8 kv heads of 128): two chunks of 1500..2048 rows
+// over 4096..8192 keys, 626 GFLOP.  NVFP4: 690..750 us a call by card (836..907
+// TFLOP/s; a large bf16 library product: 1230), under a kernel trace, at a lower
+// clock, 736..764 for this kernel.  There MXFP4 takes 807 us and affine, with one
+// workgroup per CU, 1640.  NVFP4: matrix units 43 % busy, vector issue 62 %, no
+// LDS bank conflicts; bound by the vector work beside the products.
+// Affine at D = 256 spills 204 registers.
 #include <algorithm>
 
 #include "kv_device.hpp"
@@ -38,16 +41,18 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 constexpr int kBlock = kPromptRows;
 constexpr int kTile = 64;      // keys
 // All in tiles.  Each was measured on both sides (us, this kernel + join; A: two
-// prompts of 60..120 over 541..4335 keys, affine, 8 heads over 1; B: one of
-// 611..1222 over 299..2399, MXFP4, 8 over 8; C: one of 547..1094, window 121, 32
-// over 4; D: two of 89..178 over 953..7631, 128 over 8).
-// The shortest run.  2: A 20.5 + 10.7, B 37.6 + 11.3; 4: A 24.8 + 9.6, B 37.4 +
-// 11.1; 8: A 35.5 + 6.5, B 41.9 + 8.2.
+// prompts of up to 87 rows over 1356 and 2353 keys, affine, 8 heads over 1; B: one
+// of 900 over 1300, MXFP4, 8 over 8; C: one of 341 over 2818, MXFP4, 8 over 1; D:
+// two of up to 163 over 3697 and 6397, NVFP4, 128 over 8).
+// The shortest run.  2: A 21.2 + 10.7, B 26.2 + 10.2, C 24.4 + 13.6; 4: A 25.7 +
+// 9.8, B 28.4 + 8.8, C 27.9 + 13.0; D 143.9 + 13.8 and 143.4 + 13.7.
 constexpr int kMinRun = 2;
-// The longest segment that is never cut.  8 and 4 alike (B 37.4 and 38.2); 16: B 57.7.
+// The longest segment that is never cut.  8: B 26.2 + 10.2; 4: 26.1 + 10.4; 16:
+// 45.0 + 8.9; the others alike with all three.
 constexpr int kWhole = 8;
-// What a segment costs beside its tiles.  3: C 22.7 + 3.9, D 146.9 + 14.1; 0: C
-// 34.7 + 4.3, D 152.1 + 17.0; 8: C 21.4 + 3.8, D 151.1 + 14.2.
+// What a segment costs beside its tiles.  3: A 21.2 + 10.7, B 26.2 + 10.2, C 24.4
+// + 13.6; 0: A 25.4 + 11.7, B 28.3 + 46.9, C 30.3 + 16.5; 8: A 22.7 + 10.6, B 24.3
+// + 24.5, C 26.0 + 15.0.
 constexpr int kSegment = 3;
 
 template <int D>
@@ -71,7 +76,7 @@ __device__ __forceinline__ f32x16_t mma32_f16(u32x4_t a, u32x4_t b, f32x16_t c) 
                                                 __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 // o += v (hi + lo)^T, bf16; by hand as in kv_attention.hip (58 registers spilled
-// at MXFP4, D = 128), with 32 cycles until the sums are there.
+// at MXFP4, D = 128), with 32 steps until the sums are there.
 __device__ __forceinline__ void add_wide(f32x16_t& o, u32x4_t v, u32x4_t hi, u32x4_t lo) {
   asm volatile(
       "s_nop 7\n\t"

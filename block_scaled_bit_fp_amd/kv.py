@@ -4,6 +4,8 @@
     batch = kv_plan(past_lens, q_lens, block_table, free_pages, free_begin, tokens, page_size=64)
     kv_append(cache, k, v, batch.slots)          # quantize the new rows into their pages
     out = kv_attention(q, cache, batch)          # [tokens, heads, head_dim] bf16
+    past_lens.copy_(batch.next_lens)             # what each request has in the cache now
+    free_begin.copy_(batch.state[:1])
 
 One plan serves every layer of a step; each layer has a cache of its own.
 """

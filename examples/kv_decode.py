@@ -55,8 +55,8 @@ class Block:
         self.begin = torch.zeros(1, dtype=torch.int32, device="cuda")
 
     def step(self, x, q_lens, max_q, workspace):
-        """The new tokens' hidden states x [tokens, hidden] through the block; returns (y, batch).
-        q_lens: new tokens of each request (device int32), at most max_q."""
+        """The new tokens' hidden states x [tokens, hidden] through the block; returns (y, batch, the
+        attention's output).  q_lens: new tokens of each request (device int32), at most max_q."""
         T, h = x.shape[0], self.normed(x)
         batch = bs.kv_plan(self.lens, q_lens, self.table, self.free, self.begin, tokens=T,
                            page_size=self.cache.page_size)

@@ -440,12 +440,16 @@ bsfp_status bsfp_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* 
  *   out [tokens, heads, head_dim] bf16 contiguous; lse [tokens, heads] fp32
  *   or NULL
  *   max_q: no request has more new tokens than this (host knowledge that
- *   sizes the launch; rows past it are not written)
+ *   chooses and sizes the launches; rows of a request that has more may be
+ *   left unwritten)
  *   workspace: bsfp_kv_attention_workspace_bytes(min(tokens, max_q), ...)
  *   bytes, 16-byte aligned, contents ignored; calls in flight at the same
  *   time need separate ones
  * Products run on the matrix cores with fp32 sums; maxima, sums and lse are
- * fp32.  Results are the same on every call (no atomics).
+ * fp32, probabilities and values have 11 bits.  Probabilities below 2^-40 of a
+ * row's largest count as zero, and so do MXFP4 and affine values below 2^-33 of
+ * the largest in their quarter of the head dimension among the keys that the
+ * row sees.  Results are the same on every call (no atomics).
  * Errors: BSFP_ERR_ARG for bad pointers, shapes, strides, max_q < 1, a scale
  * that is not positive or not finite times log2 e, or a small workspace;
  * BSFP_ERR_UNSUPPORTED for formats or head dimensions outside the above,
