@@ -35,6 +35,7 @@
 // Affine, 32 heads over 32, 134 MB: 41.9 us; vector issue is 59 % busy, mostly
 // with decoding, and two waves per SIMD do not cover the rest.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_device.hpp"
 
@@ -538,26 +539,30 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_split_kernel
           for (int d = 0; d < DT; ++d)
             o[d] *= ldexpf(1.0f, __builtin_amdgcn_readlane(to - nb, (d * 64 / D) * 16));
           nb = to;
+          const u32x4_t hi = wide_probabilities<false>(pf), lo = wide_probabilities<true>(pf);
+          auto add = [&](auto rest) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const Words<W> w =
-                load_codes<D>(p.v.codes + max(rows_now.row[u], (int64_t)0) * (D / 2), n, qd);
+            for (int u = 0; u < 2; ++u) {
+              const Words<W> w =
+                  load_codes<D>(p.v.codes + max(rows_now.row[u], (int64_t)0) * (D / 2), n, qd);
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-              *reinterpret_cast<u32x4_t*>(vt + (u * 16 + n) * v_stride<D>() + qd * (D / 4) + j * 8) =
-                  large[u] ? decode_value_wide<MODE, D>(w.w[j], scales[u], j, nb)
-                           : u32x4_t{0, 0, 0, 0};
+              for (int j = 0; j < W; ++j) {
+                *reinterpret_cast<u32x4_t*>(vt + (u * 16 + n) * v_stride<D>() + qd * (D / 4) + j * 8) =
+                    large[u] ? decode_value_wide<MODE, D, decltype(rest)::value>(w.w[j], scales[u], j, nb)
+                             : u32x4_t{0, 0, 0, 0};
+                step_end();
+              }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              add_wide(o[d], value_operand(d), hi, lo);
               step_end();
             }
-          }
-          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-          const u32x4_t hi = wide_probabilities<false>(pf), lo = wide_probabilities<true>(pf);
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            add_wide(o[d], value_operand(d), hi, lo);
-            step_end();
-          }
-          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          };
+          add(std::false_type{});
+          if constexpr (MODE == BSFP_AFFINE) add(std::true_type{});
         }
       }
     };

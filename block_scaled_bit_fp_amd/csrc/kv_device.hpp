@@ -270,8 +270,8 @@ __device__ __forceinline__ int value_shift(int e) { return min(kValueExp - e, 12
 // tile out of fp16.  Where the exponents of a tile that some rows do not see
 // whole pass the present scale by kValueSpread, the quarters of rows that do not
 // fit it are left out at first and then added by themselves: as bf16, which has
-// the range (exact for MXFP4; affine ones keep 8 bits), with the probabilities
-// as the sum of two bf16.  nb then falls only as far as it must for fp32:
+// the range (exact for MXFP4, the sum of two for affine), with the probabilities
+// as the sum of two.  nb then falls only as far as it must for fp32:
 // products of probabilities with values up to 2^115; still larger values are
 // finite themselves, so that a probability of zero takes them out.
 constexpr int kValueSpread = 12, kValueExpWide = 230, kValueExpTop = 242;
@@ -292,8 +292,9 @@ __device__ __forceinline__ u32x4_t wide_probabilities(u32x4_t p) {
   }
   return o;
 }
-// Values: word j as four bf16 pairs, times 2^nb.
-template <int MODE, int D>
+// Values: word j as four bf16 pairs, times 2^nb; REST: what that leaves of
+// affine ones (MXFP4 ones are exact).
+template <int MODE, int D, bool REST>
 __device__ __forceinline__ u32x4_t decode_value_wide(uint32_t w, uint32_t scales, int j, int nb) {
   u32x4_t o;
   if constexpr (MODE == BSFP_MXFP4) {
@@ -306,7 +307,11 @@ __device__ __forceinline__ u32x4_t decode_value_wide(uint32_t w, uint32_t scales
     const float s = ldexpf(bf16_lo(scales), nb), b = ldexpf(bf16_hi(scales), nb);
     auto value = [&](int i) { return __builtin_fmaf((float)(w >> (4 * i) & 15u), s, b); };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(value(2 * i), value(2 * i + 1));
+    for (int i = 0; i < 4; ++i) {
+      const float x = value(2 * i), y = value(2 * i + 1);
+      const uint32_t hi = pack_bf16x2(x, y);
+      o[i] = REST ? pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi)) : hi;
+    }
   }
   return o;
 }

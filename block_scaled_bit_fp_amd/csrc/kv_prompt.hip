@@ -27,8 +27,9 @@
 // clock, 736..764 for this kernel.  There MXFP4 takes 807 us and affine, with one
 // workgroup per CU, 1640.  NVFP4: matrix units 43 % busy, vector issue 62 %, no
 // LDS bank conflicts; bound by the vector work beside the products.
-// Affine at D = 256 spills 204 registers.
+// Affine at D = 256 spills 497 registers, most of them on the rare paths.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_device.hpp"
 
@@ -672,22 +673,24 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
           int to[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) to[x] = value_shift_wide(nb_now[x], largest(s_exp[at][x]));
-          __syncthreads();  // all waves are done with the tile
-          const int key = key0 + skey;
-          Row<D> r;
-          load_row<MODE, D>(p, p.v, head, key, page_of(t), sq, r);
+          if (any_seen) rescale(to);
           const int nb = own(nb_now[0], nb_now[1], nb_now[2], nb_now[3]);
           const int nb_wide = own(to[0], to[1], to[2], to[3]);
-          const bool large = r.ok && key >= all.any_lo && key < all.any_hi &&
-                             !not_finite<MODE>(r.s) && value_exponent<MODE, D>(r.s) + nb > kValueExpMax;
-          uint16_t* row = buf.v[at] + skey * v_stride<D>() + sq * (D / 4);
+          auto add = [&](auto rest) {
+            __syncthreads();  // all waves are done with the tile as it is
+            const int key = key0 + skey;
+            Row<D> r;
+            load_row<MODE, D>(p, p.v, head, key, page_of(t), sq, r);
+            const bool large = r.ok && key >= all.any_lo && key < all.any_hi &&
+                               !not_finite<MODE>(r.s) && value_exponent<MODE, D>(r.s) + nb > kValueExpMax;
+            uint16_t* row = buf.v[at] + skey * v_stride<D>() + sq * (D / 4);
 #pragma unroll
-          for (int j = 0; j < W; ++j)
-            *reinterpret_cast<u32x4_t*>(row + v_piece<D>(sq, j) * 8) =
-                large ? decode_value_wide<MODE, D>(r.w.w[j], r.s, j, nb_wide) : u32x4_t{0, 0, 0, 0};
-          __syncthreads();
-          if (any_seen) {
-            rescale(to);
+            for (int j = 0; j < W; ++j)
+              *reinterpret_cast<u32x4_t*>(row + v_piece<D>(sq, j) * 8) =
+                  large ? decode_value_wide<MODE, D, decltype(rest)::value>(r.w.w[j], r.s, j, nb_wide)
+                        : u32x4_t{0, 0, 0, 0};
+            __syncthreads();
+            if (!any_seen) return;
             // the probabilities once more: keeping them would take registers in
             // every tile
             f32x16_t sc[2];
@@ -722,7 +725,9 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(MODE, D)) void kv_prompt_kerne
                 step_end();
               }
             }
-          }
+          };
+          add(std::false_type{});
+          if constexpr (kAffine) add(std::true_type{});
         }
       }
       publish(rv, t + 2, false);

@@ -151,8 +151,8 @@ def put(bsfp, cache, batch, r, t, P, v):
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_huge_values_reach_only_the_rows_that_see_them(bsfp, mode, size, kv, q_lens, heads, window, D):
     """Two new tokens, one of them a million times larger, with values far beyond the others': rows that do not
-    see them are, within the tolerance, those over the values that they do see; the huge ones themselves come
-    through to the rows that see them, to 7 bits."""
+    see them are, within the tolerance, those over the values that they do see; to the rows that see them the
+    huge ones come through."""
     P, scale = 32, float(np.float32(1.0 / np.sqrt(D)))
     cols = [7, D - 28]
     cache, batch, q = build(bsfp, mode, kv, q_lens, heads, 1, D, P, seed=heads + q_lens[0])
@@ -170,8 +170,7 @@ def test_huge_values_reach_only_the_rows_that_see_them(bsfp, mode, size, kv, q_l
     assert not torch.isnan(lse).any() and not sees.all() and sees.any()
     if size <= 1e30:
         want, _, tol, _ = ref.attention(q, cache, batch.block_table, batch.kv_lens, batch.q_starts, scale, window)
-        # the tolerance holds 2^-11 of the sum of probabilities times |V| at least
-        assert (np.abs(got - want)[sees][..., cols] <= 16 * tol[sees][..., cols]).all()
+        assert (np.abs(got - want)[sees][..., cols] <= tol[sees][..., cols]).all()
     # the reference over a cache in which those keys' values are small ones, and the same keys
     for r, t, _ in huge:
         put(bsfp, cache, batch, r, t, P, rand((1, 1, D), t))
